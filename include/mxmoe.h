@@ -486,6 +486,148 @@ int moe_layer_bwd_q(const void* dout_tokens, int64_t T, int64_t D, const float* 
                     const mxmoe_layer_saved* saved, void* dx_tokens, void* dw13, void* dw2, float* dweights,
                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * Operators beside the MXFP8 path (no counterpart in the source pages).
+ * 16-bit tensors are bfloat16 or IEEE half: dtype = MXMOE_BF16 / MXMOE_FP16
+ * for every 16-bit tensor of a call.
+ * ------------------------------------------------------------------------- */
+#define MXMOE_BF16 0
+#define MXMOE_FP16 1
+
+/* -------------------------------------------------------------------------
+ * mxmoe_ragged_gemm -- grouped product over ragged segments, 16-bit operands.
+ *
+ *  transpose_w 0:  out[m, n] = sum_k a[m, k] * W[e, n, k]   a [M, K], out [M, N]
+ *  transpose_w 1:  out[m, k] = sum_n a[m, n] * W[e, n, k]   a [M, N], out [M, K]
+ *  for offsets[e] <= m < offsets[e+1]; the second form is the first one's input
+ *  gradient.  fp32 accumulation, one rounding.  w is [E, N, K].
+ *
+ *  expert_offsets  DEVICE int32 [E+1], offsets[0] == 0, non-decreasing,
+ *                  offsets[E] <= M; segments of any length at any row (no
+ *                  padding), e.g. mxmoe_route with pad_multiple = 1.  A bad
+ *                  table writes nothing and raises MXMOE_ERR_OFFSETS in
+ *                  mxmoe_check_device_error().
+ *  Rows at or past offsets[E] are not written, and what they hold (NaN, say)
+ *  has no effect.  out must not overlap a or w.
+ *  Needs N and K multiples of 8, E <= 1024, 0 <= M < 2^31 (M == 0: nothing is
+ *  done), 16-byte aligned tensors.
+ * ------------------------------------------------------------------------- */
+int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N, int64_t K,
+                      const int32_t* expert_offsets, int transpose_w, int dtype, void* out, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * mxmoe_ragged_gemm_wgrad -- weight gradient of mxmoe_ragged_gemm.
+ *
+ *  dw[e, n, k] = sum over m in expert e's segment of g[m, n] * a[m, k]
+ *  g [M, N], a [M, K], dw [E, N, K]; fp32 accumulation, one rounding.  Every
+ *  expert's gradient is written; one without rows gets exact zeros (M == 0:
+ *  all of them).  Segments and limits as mxmoe_ragged_gemm.
+ * ------------------------------------------------------------------------- */
+int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, int64_t M,
+                            const int32_t* expert_offsets, int E, int dtype, void* dw, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * mxfp8_swiglu_ckpt -- SwiGLU that keeps its input in 8 bits.
+ *
+ *  h13 [rows, 2F] = [a | b];  h = silu(a) * b  [rows, F], computed in fp32 from
+ *  the 16-bit h13 and rounded once.
+ *  codes  uint8 [rows, 2F], scales uint8 [rows, 2, ceil(F/32)]: h13 as MXFP8
+ *         (E4M3, the scale rule above), blocks of 32 along each half, the last
+ *         one of a half short when F % 32 != 0.  With F % 32 == 0 these are
+ *         mxfp8_quantize's ROW codes and PLAIN scales of h13.
+ *  rows_dev  DEVICE int32 (may be NULL), e.g. offsets + E: rows at or past
+ *            *rows_dev are neither read nor written.
+ *  Needs F % 8 == 0 and 16-byte aligned h13, h and codes; rows >= 0.
+ * ------------------------------------------------------------------------- */
+int mxfp8_swiglu_ckpt(const void* h13, int64_t rows, int64_t F, const int32_t* rows_dev, int dtype, void* h,
+                      uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* Backward of mxfp8_swiglu_ckpt from the kept copy: with a, b the decoded
+ * values and s = 1 / (1 + e^-a), in fp32 with one rounding per output,
+ *   dh13 [rows, 2F] = [dh * b * s * (1 + a * (1 - s)) | dh * a * s]
+ *   h    [rows, F]  = a * s * b     (the second weight's gradient operand; may be NULL)
+ * dh [rows, F].  A block that held NaN or infinity decodes to NaN. */
+int mxfp8_swiglu_ckpt_bwd(const void* dh, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t F,
+                          const int32_t* rows_dev, int dtype, void* dh13, void* h, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * MXFP4 weights: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit), two a
+ * byte, with one E8M0 scale byte per 32 columns.  Scale rule (OCP MX v1.0):
+ * byte = clamp(floor(log2(amax)) - 2 + 127, 0, 254); elements round to
+ * nearest-even E2M1 and saturate at +-6; a block holding NaN/Inf gets byte
+ * 0xFF, which decodes to NaN.
+ *
+ * Layouts of a weight [E, rows, cols] (one expert after the other):
+ *  MXFP4_PLAIN  codes [E, rows, cols/2], the even column in the low four bits;
+ *               scales [E, rows, cols/32].
+ *  MXFP4_TILE   for the matvec: cells of 16 rows x 128 columns, cell (t, c) of
+ *               an expert (rows 16t.., columns 128c..) at byte
+ *               (t * cols/128 + c) * 1024 of its codes.  In a cell the four
+ *               bytes (eight columns) of row 8h + g, columns 32j + 8q.. sit at
+ *               512h + 64g + 16q + 4j; scales: (t * cols/128 + c) * 64 +
+ *               4 * row + j.
+ *  MXFP4_TILE_GATED  the same for W13 [E, 2F, D]: cell row t takes the gate rows
+ *               8t..8t+7 as its rows 0..7 and the up rows F + 8t.. as 8..15.
+ * ------------------------------------------------------------------------- */
+#define MXFP4_PLAIN 0
+#define MXFP4_TILE 1
+#define MXFP4_TILE_GATED 2
+
+/* x [batch, rows, cols] 16-bit -> codes (batch*rows*cols/2 bytes), scales
+ * (batch*rows*cols/32 bytes).  PLAIN needs cols % 32 == 0, the tile layouts
+ * cols % 128 == 0 and rows % 16 == 0; 16-byte aligned buffers. */
+int mxfp4_quantize(const void* x, int64_t batch, int64_t rows, int64_t cols, int dtype, int layout, uint8_t* codes,
+                   uint8_t* scales, cudaStream_t stream);
+
+/* PLAIN codes and scales of [rows, cols] -> 16-bit values (code * 2^(byte-127),
+ * rounded once), cols % 32 == 0. */
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int dtype, void* out,
+                     cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * mxfp4_expert_matvec -- routed matrix-vector products with 4-bit weights.
+ *
+ *  y[s, n] = sum_k W[expert_ids[s], n, k] * x[s, k],  s < S
+ *  x [S, K], y [S, N] 16-bit; weights [E, N, K] in the MXFP4_TILE layout;
+ *  expert_ids DEVICE int32 [S] in [0, E) (any order, repeats allowed; an id
+ *  outside raises MXMOE_ERR_ARG on the device and its row of y is not
+ *  written).  Each expert's weights are read once per eight slots it has (fewer
+ *  for K above 7168, as shared memory allows).  Products with f16 copies of x (a power of two per row keeps 16-bit inputs
+ *  exact down to 2^-36 of the row's largest value), fp32 sums, one rounding.
+ *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048.
+ * ------------------------------------------------------------------------- */
+int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expert_ids, const uint8_t* codes,
+                        const uint8_t* scales, int E, int64_t N, int dtype, void* y, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_layer_decode_fp4 -- a routed-experts layer on 4-bit weights for one to a
+ * few tokens (the serving form of moe_layer_fwd_q):
+ *
+ *  out[t] = sum_j topk_weights[t, j] * W2[e] . (silu(gate) * up),
+ *  [gate | up] = W13[e] . x[t],  e = topk_ids[t, j]
+ *
+ *  x_tokens, out_tokens [T, D] 16-bit; topk_ids int32 and topk_weights fp32
+ *  [T, top_k] on the device; an id outside [0, E) raises MXMOE_ERR_ARG there and
+ *  adds nothing.  gate, up, h, the experts' outputs and the weighted sum are
+ *  held in fp32 (h enters its product as f16, scaled by a power of two per
+ *  slot); one rounding at the end.
+ *  Needs D and F multiples of 128, T * top_k <= 2048, top_k <= E <= 1024.
+ *  Workspace: mxfp4_decode_workspace_size() bytes, not shared by calls that
+ *  may overlap on the GPU.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* w13_codes;     /* W13 [E, 2F, D] in MXFP4_TILE_GATED */
+  uint8_t* w13_scales;
+  uint8_t* w2_codes;      /* W2 [E, D, F] in MXFP4_TILE */
+  uint8_t* w2_scales;
+} mxmoe_q4weights;
+
+size_t mxfp4_decode_workspace_size(int64_t T, int top_k, int64_t D, int64_t F);
+
+int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32_t* topk_ids,
+                         const float* topk_weights, int top_k, const mxmoe_q4weights* qw, int E, int64_t F, int dtype,
+                         void* out_tokens, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

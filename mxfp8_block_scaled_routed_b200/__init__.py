@@ -23,10 +23,13 @@ __all__ = [
     "make_qweights", "mxmoe_quantize_weights", "moe_mlp_fwd_q", "moe_mlp_bwd_q", "moe_mlp_fwd_unfused_q",
     "mxmoe_route_capacity", "mxmoe_route", "mxmoe_permute_quant", "mxmoe_unpermute_combine",
     "mxmoe_combine_weight_grad", "make_layer_saved", "moe_layer_fwd_q", "moe_layer_bwd_q",
+    "TILE", "TILE_GATED", "mxmoe_ragged_gemm", "mxmoe_ragged_gemm_wgrad", "mxfp8_swiglu_ckpt", "mxfp8_swiglu_ckpt_bwd",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_expert_matvec", "mxfp4_quantize_experts", "moe_layer_decode_fp4",
 ]
 
 ROW, COL = 1, 2
 PLAIN, MMA = 0, 1
+TILE, TILE_GATED = 1, 2        # layouts of 4-bit weights (beside PLAIN)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxmoe.so")
@@ -52,6 +55,10 @@ class _QWeights(ctypes.Structure):
 class _LayerSaved(ctypes.Structure):
     _fields_ = [("offsets", ctypes.c_void_p), ("row_slot", ctypes.c_void_p), ("slot_row", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("mlp", _Saved)]
+
+
+class _Q4Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w13_codes", "w13_scales", "w2_codes", "w2_scales")]
 
 
 _P, _I, _L, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -91,6 +98,15 @@ _SIGS = {
                          ctypes.POINTER(_LayerSaved), _P, _S, _P], _I),
     "moe_layer_bwd_q": ([_P, _L, _L, _P, _I, ctypes.POINTER(_QWeights), _I, _L, _I, ctypes.POINTER(_LayerSaved),
                          _P, _P, _P, _P, _P, _S, _P], _I),
+    "mxmoe_ragged_gemm": ([_P, _L, _P, _I, _L, _L, _P, _I, _I, _P, _P], _I),
+    "mxmoe_ragged_gemm_wgrad": ([_P, _L, _P, _L, _L, _P, _I, _I, _P, _P], _I),
+    "mxfp8_swiglu_ckpt": ([_P, _L, _L, _P, _I, _P, _P, _P, _P], _I),
+    "mxfp8_swiglu_ckpt_bwd": ([_P, _P, _P, _L, _L, _P, _I, _P, _P, _P], _I),
+    "mxfp4_quantize": ([_P, _L, _L, _L, _I, _I, _P, _P, _P], _I),
+    "mxfp4_dequantize": ([_P, _P, _L, _L, _I, _P, _P], _I),
+    "mxfp4_expert_matvec": ([_P, _L, _L, _P, _P, _P, _I, _L, _I, _P, _P], _I),
+    "mxfp4_decode_workspace_size": ([_L, _I, _L, _L], _S),
+    "moe_layer_decode_fp4": ([_P, _L, _L, _P, _P, _I, ctypes.POINTER(_Q4Weights), _I, _L, _I, _P, _P, _S, _P], _I),
 }
 
 _lib = None
@@ -593,3 +609,209 @@ def moe_layer_bwd_q(dout_tokens, topk_weights, qw, saved, pad_multiple=256, dx=N
                                  ctypes.byref(st), _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(dwr), _ptr(ws), ws.numel(),
                                  _stream(dout_tokens)))
     return dx, dw13, dw2, dwr
+
+
+# ----------------------------------------------------------------------------- operators beside the MXFP8 path
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _dtype(t, name: str) -> int:
+    """Code of a 16-bit float CUDA tensor's type (contiguous, on the GPU)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    _need(t, t.dtype, name)
+    return code
+
+
+def _like(t, ref, shape, dtype, name: str):
+    """t checked against a shape, a type and ref's device; None allocates it there."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    _need(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+    return t
+
+
+def _call(fn, ref, *args):
+    """fn(*args, stream) on ref's device and that device's current stream."""
+    i = ref.get_device()
+    if i == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(i).cuda_stream))
+    else:
+        with torch.cuda.device(i):
+            _check(fn(*args, torch.cuda.current_stream(i).cuda_stream))
+
+
+def mxmoe_ragged_gemm(a, w, offsets, transpose_w=False, out=None):
+    """Grouped product over ragged segments (bf16 or fp16, no padding).
+
+    a [M, K], w [E, N, K], offsets int32 [E + 1] on the device:
+    out[m] = a[m] . w[e]^T for offsets[e] <= m < offsets[e + 1], [M, N].
+    transpose_w=True is its input gradient: a [M, N], out[m] = a[m] . w[e], [M, K].
+    Rows at or past offsets[E] are not written (a fresh out holds arbitrary values there).
+    """
+    dt = _dtype(a, "a")
+    if a.dim() != 2:
+        raise ValueError("a must be 2-D")
+    _like(offsets, a, offsets.shape, torch.int32, "offsets")
+    E = offsets.numel() - 1
+    if w.dim() != 3 or w.shape[0] != E or w.shape[1 if transpose_w else 2] != a.shape[1]:
+        raise ValueError(f"w must be [E={E}, N, K] with {'N' if transpose_w else 'K'}={a.shape[1]}, got {tuple(w.shape)}")
+    _like(w, a, w.shape, a.dtype, "w")
+    M, (_, N, K) = a.shape[0], w.shape
+    out = _like(out, a, (M, K if transpose_w else N), a.dtype, "out")
+    _call(lib().mxmoe_ragged_gemm, a, a.data_ptr(), M, w.data_ptr(), E, N, K, offsets.data_ptr(), int(bool(transpose_w)),
+          dt, out.data_ptr())
+    return out
+
+
+def mxmoe_ragged_gemm_wgrad(g, a, offsets, out=None):
+    """Weight gradient of mxmoe_ragged_gemm: g [M, N], a [M, K] -> dw [E, N, K], dw[e] = g_e^T . a_e.
+
+    An expert without rows gets exact zeros."""
+    dt = _dtype(g, "g")
+    if g.dim() != 2 or a.dim() != 2:
+        raise ValueError("g and a must be 2-D")
+    M, N = g.shape
+    K = a.shape[1]
+    _like(a, g, (M, K), g.dtype, "a")
+    _like(offsets, g, offsets.shape, torch.int32, "offsets")
+    E = offsets.numel() - 1
+    out = _like(out, g, (E, N, K), g.dtype, "out")
+    _call(lib().mxmoe_ragged_gemm_wgrad, g, g.data_ptr(), N, a.data_ptr(), K, M, offsets.data_ptr(), E, dt,
+          out.data_ptr())
+    return out
+
+
+def mxfp8_swiglu_ckpt(h13, rows_dev=None, h=None, codes=None, scales=None):
+    """SwiGLU that keeps its input in 8 bits: h13 [rows, 2F] (bf16 or fp16) -> dict(h, codes, scales).
+
+    h [rows, F] = silu(gate) * up; codes [rows, 2F] and scales [rows, 2, ceil(F/32)] are h13 as MXFP8 (E4M3),
+    blocks of 32 along each half.  rows_dev (int32 on the device, e.g. offsets[E:]): rows at or past it are left alone.
+    """
+    dt = _dtype(h13, "h13")
+    if h13.dim() != 2 or h13.shape[1] % 2:
+        raise ValueError("h13 must be [rows, 2F]")
+    rows, F = h13.shape[0], h13.shape[1] // 2
+    if rows_dev is not None:
+        _like(rows_dev, h13, (1,), torch.int32, "rows_dev")
+    h = _like(h, h13, (rows, F), h13.dtype, "h")
+    codes = _like(codes, h13, (rows, 2 * F), torch.uint8, "codes")
+    scales = _like(scales, h13, (rows, 2, (F + 31) // 32), torch.uint8, "scales")
+    _call(lib().mxfp8_swiglu_ckpt, h13, h13.data_ptr(), rows, F, None if rows_dev is None else rows_dev.data_ptr(), dt,
+          h.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return dict(h=h, codes=codes, scales=scales)
+
+
+def mxfp8_swiglu_ckpt_bwd(dh, codes, scales, rows_dev=None, dh13=None, h=None, want_h=True):
+    """Backward of mxfp8_swiglu_ckpt from the kept copy: dh [rows, F] -> dict(dh13 [rows, 2F], h [rows, F] or None).
+
+    h is recomputed from the kept copy (the operand of the second weight's gradient)."""
+    dt = _dtype(dh, "dh")
+    if dh.dim() != 2:
+        raise ValueError("dh must be 2-D")
+    rows, F = dh.shape
+    _like(codes, dh, (rows, 2 * F), torch.uint8, "codes")
+    _like(scales, dh, (rows, 2, (F + 31) // 32), torch.uint8, "scales")
+    if rows_dev is not None:
+        _like(rows_dev, dh, (1,), torch.int32, "rows_dev")
+    dh13 = _like(dh13, dh, (rows, 2 * F), dh.dtype, "dh13")
+    if want_h or h is not None:
+        h = _like(h, dh, (rows, F), dh.dtype, "h")
+    _call(lib().mxfp8_swiglu_ckpt_bwd, dh, dh.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, F,
+          None if rows_dev is None else rows_dev.data_ptr(), dt, dh13.data_ptr(), None if h is None else h.data_ptr())
+    return dict(dh13=dh13, h=h)
+
+
+def mxfp4_quantize(w, layout: int = PLAIN):
+    """bf16 or fp16 [rows, cols] or [E, rows, cols] -> dict(codes [.., rows, cols/2], scales [.., rows, cols/32]).
+
+    E2M1 codes, two a byte, with one E8M0 byte per 32 columns.  PLAIN keeps the matrix order; TILE and TILE_GATED
+    are the orders that mxfp4_expert_matvec and moe_layer_decode_fp4 read (same shapes, cells of 16 rows x 128 columns)."""
+    dt = _dtype(w, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be 2-D or 3-D")
+    E = w.shape[0] if w.dim() == 3 else 1
+    rows, cols = w.shape[-2], w.shape[-1]
+    codes = _u8((*w.shape[:-1], cols // 2), w.device)
+    scales = _u8((*w.shape[:-1], cols // 32), w.device)
+    _call(lib().mxfp4_quantize, w, w.data_ptr(), E, rows, cols, dt, layout, codes.data_ptr(), scales.data_ptr())
+    return dict(codes=codes, scales=scales)
+
+
+def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16):
+    """MXFP4 (PLAIN) -> bf16 or fp16: codes [.., cols/2], scales [.., cols/32] -> [.., cols]."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    _need(codes, torch.uint8, "codes")
+    if codes.dim() not in (2, 3):
+        raise ValueError("codes must be 2-D or 3-D")
+    cols = 2 * codes.shape[-1]
+    rows = codes.shape[-2] * (codes.shape[0] if codes.dim() == 3 else 1)
+    _like(scales, codes, (*codes.shape[:-1], cols // 32), torch.uint8, "scales")
+    out = torch.empty((*codes.shape[:-1], cols), dtype=dtype, device=codes.device)
+    _call(lib().mxfp4_dequantize, codes, codes.data_ptr(), scales.data_ptr(), rows, cols, _DTYPES[dtype], out.data_ptr())
+    return out
+
+
+def mxfp4_expert_matvec(x, expert_ids, codes, scales, out=None):
+    """Routed matrix-vector products with 4-bit weights: y[s] = W[expert_ids[s]] . x[s].
+
+    x [S, K] bf16 or fp16, expert_ids int32 [S], codes [E, N, K/2] and scales [E, N, K/32] in the TILE layout; y [S, N].
+    For a few slots (at most 2048): each expert's weights are read once per eight of its slots."""
+    dt = _dtype(x, "x")
+    if x.dim() != 2 or codes.dim() != 3:
+        raise ValueError("x must be [S, K] and codes [E, N, K/2]")
+    S, K = x.shape
+    E, N = codes.shape[:2]
+    _like(expert_ids, x, (S,), torch.int32, "expert_ids")
+    _like(codes, x, (E, N, K // 2), torch.uint8, "codes")
+    _like(scales, x, (E, N, K // 32), torch.uint8, "scales")
+    out = _like(out, x, (S, N), x.dtype, "out")
+    _call(lib().mxfp4_expert_matvec, x, x.data_ptr(), S, K, expert_ids.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          E, N, dt, out.data_ptr())
+    return out
+
+
+def mxfp4_quantize_experts(w13, w2):
+    """4-bit copies of W13 [E, 2F, D] and W2 [E, D, F] in the layouts that moe_layer_decode_fp4 reads."""
+    if w13.dim() != 3 or w2.dim() != 3 or w13.shape != (w2.shape[0], 2 * w2.shape[2], w2.shape[1]):
+        raise ValueError(f"w13 must be [E, 2F, D] and w2 [E, D, F], got {tuple(w13.shape)} and {tuple(w2.shape)}")
+    a, b = mxfp4_quantize(w13, TILE_GATED), mxfp4_quantize(w2, TILE)
+    return dict(w13_codes=a["codes"], w13_scales=a["scales"], w2_codes=b["codes"], w2_scales=b["scales"])
+
+
+def moe_layer_decode_fp4(x_tokens, topk_ids, topk_weights, qw, out=None, workspace=None):
+    """Routed-experts layer on 4-bit weights for one to a few tokens (T * top_k <= 2048).
+
+    x_tokens [T, D] bf16 or fp16, topk_ids int32 and topk_weights fp32 [T, top_k], qw from mxfp4_quantize_experts:
+    out[t] = sum_j topk_weights[t, j] * W2[e] . (silu(gate) * up), [gate | up] = W13[e] . x[t], e = topk_ids[t, j].
+    workspace (optional): uint8, at least mxfp4_decode_workspace_size bytes; calls that may overlap need one each."""
+    dt = _dtype(x_tokens, "x_tokens")
+    if x_tokens.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("x_tokens must be [T, D] and topk_ids [T, top_k]")
+    T, D = x_tokens.shape
+    k = topk_ids.shape[1]
+    c13, c2 = qw["w13_codes"], qw["w2_codes"]
+    E, F = c13.shape[0], c13.shape[1] // 2
+    _like(topk_ids, x_tokens, (T, k), torch.int32, "topk_ids")
+    _like(topk_weights, x_tokens, (T, k), torch.float32, "topk_weights")
+    _like(c13, x_tokens, (E, 2 * F, D // 2), torch.uint8, "qw['w13_codes']")
+    _like(c2, x_tokens, (E, D, F // 2), torch.uint8, "qw['w2_codes']")
+    _like(qw["w13_scales"], x_tokens, (E, 2 * F, D // 32), torch.uint8, "qw['w13_scales']")
+    _like(qw["w2_scales"], x_tokens, (E, D, F // 32), torch.uint8, "qw['w2_scales']")
+    out = _like(out, x_tokens, (T, D), x_tokens.dtype, "out")
+    if workspace is None:
+        workspace = _u8((lib().mxfp4_decode_workspace_size(T, k, D, F),), x_tokens.device)
+    else:
+        _like(workspace, x_tokens, workspace.shape, torch.uint8, "workspace")
+    st = _Q4Weights(c13.data_ptr(), qw["w13_scales"].data_ptr(), c2.data_ptr(), qw["w2_scales"].data_ptr())
+    _call(lib().moe_layer_decode_fp4, x_tokens, x_tokens.data_ptr(), T, D, topk_ids.data_ptr(), topk_weights.data_ptr(), k,
+          ctypes.byref(st), E, F, dt, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out

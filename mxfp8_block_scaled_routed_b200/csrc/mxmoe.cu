@@ -1,13 +1,17 @@
 // libmxmoe: C ABI of the MXFP8 routed-experts MLP (declared in include/mxmoe.h).
 //
 // One translation unit: the cast kernels (quant.cuh), the tcgen05 grouped
-// GEMM (gemm.cuh), the token dispatcher (route.cuh) and the host code below,
-// which validates every argument, encodes the TMA tensor maps, launches on
-// the caller's stream and chains the composites.  Nothing here calls a
+// GEMM (gemm.cuh), the token dispatcher (route.cuh), the operators beside the
+// MXFP8 path (16-bit ragged products in ragged.cuh, the SwiGLU checkpoint in
+// ckpt.cuh, 4-bit weights in fp4.cuh, their host side in host16.cuh) and the
+// host code below, which validates every argument, encodes the TMA tensor
+// maps, launches on the caller's stream and chains the composites.  Nothing here calls a
 // device allocator.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +21,9 @@
 #include "gemm.cuh"
 #include "quant.cuh"
 #include "route.cuh"
+#include "ckpt.cuh"
+#include "fp4.cuh"
+#include "ragged.cuh"
 
 using namespace mxmoe;
 
@@ -1246,3 +1253,5 @@ int moe_layer_bwd_q(const void* dout_tokens, int64_t T, int64_t D, const float* 
 }
 
 }  // extern "C"
+
+#include "host16.cuh"
