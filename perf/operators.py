@@ -244,7 +244,7 @@ def run(st):
         if op == "ckpt":
             f = mxk.mxfp8_swiglu_ckpt(st["h13"])
             b = mxk.mxfp8_swiglu_ckpt_bwd(st["dh"], f["codes"], f["scales"])
-            return dict(h=f["h"], codes=f["codes"].view(torch.float8_e4m3fn), scales=f["scales"], dh13=b["dh13"], h_again=b["h"])
+            return dict(h=f["h"], codes=f["codes"].view(torch.float8_e4m3fn), scales=f["scales"].flatten(1), dh13=b["dh13"], h_again=b["h"])
         if op == "decode":
             return mxk.moe_layer_decode_fp4(st["x"], st["ids"], st["weights"], st["qw"], out=st["out"])
         q = mxk.mxfp4_quantize(st["w"])
