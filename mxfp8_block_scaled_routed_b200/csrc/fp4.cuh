@@ -47,6 +47,19 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
+// Four E8M0 bytes -> fp32, exact (0 is 2^-127, 0xFF NaN): two conversions to
+// bf16 pairs, whose bits are the upper half of the fp32 ones.
+__device__ __forceinline__ void e8m0x4_to_f32(uint32_t w, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.bf16x2.ue8m0x2 %0, a; cvt.rn.bf16x2.ue8m0x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  f[0] = bf16lo_to_f32(lo);
+  f[1] = bf16hi_to_f32(lo);
+  f[2] = bf16lo_to_f32(hi);
+  f[3] = bf16hi_to_f32(hi);
+}
+
 // Byte offset of the codes (and of the scale) of row r, columns 8 c8.. in one
 // expert's matrix of R rows and K columns.
 __device__ __forceinline__ void fp4_place(int layout, int64_t r, uint32_t c8, int64_t R, int64_t K, int64_t& code,
@@ -148,14 +161,22 @@ fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restr
 // 11 bits, an eighth of the bf16 rounding of the result.
 //
 // Bound by HBM: (1/2 + 1/32) N K bytes per expert that has a slot.  A block of
-// 16 warps per SM walks a contiguous range of (slot group, row tile) units;
-// each warp takes every 16th 128-column cell of the tile through its own ring
-// of bulk copies, so the loads of later tiles are in flight while this one is
-// multiplied, and the warps' partial sums meet in shared memory in a fixed
-// order.
-constexpr int kMvThreads = 512, kMvWarps = 16;
-constexpr int kMvCell = 1024 + 64;          // codes and scales of a 16 x 128 cell
-constexpr int kMvRing = 4;                  // cells in flight per warp
+// 12 warps per SM walks a contiguous range of (slot group, row tile) units;
+// each warp takes its share of a tile's 128-column cells through its own ring
+// of cp.async loads (every lane reads back the codes it loaded itself), so the
+// loads of later tiles are in flight while this one is multiplied, and the
+// warps' partial sums meet in shared memory in a fixed order.
+// Measured on 46 of 64 experts of 7168 x 2048 (1.08 GB of weights, both
+// products and the combine): 214 us, 5.0 TB/s of weights; the loop without its
+// products 175 us.  What is left is issue (132 instructions a cell, of which
+// 32 conversions, 8 MMAs, 16 FMAs).  Bulk copies instead of cp.async: 236 us
+// (about 75 cycles of the issuing warp a copy; from one feeding warp 352 us);
+// one cell a load 228 us; 16 / 20 warps 217 / 215 us, and 2 to 3 us more on
+// one token.
+constexpr int kMvWarps = 12, kMvThreads = 32 * kMvWarps;
+constexpr int kMvCells = 2;                 // neighbouring cells (16 x 128) that a warp loads together
+constexpr int kMvRing = 3;                  // such loads in flight per warp
+constexpr int kMvSlot = kMvCells * (1024 + 64);
 constexpr int kMvMaxSlots = 2048, kMvMaxE = 1024;
 
 struct MvArgs {
@@ -166,6 +187,7 @@ struct MvArgs {
   int E;
   int64_t tiles;            // row tiles per expert
   int K;
+  int team_warps;           // warps that share a tile's cells: 1, 2, 4, 8 or 16
   int group;                // slots per group, 1..8 (shared memory holds group * K f16)
   const uint8_t* codes;
   const uint8_t* scales;
@@ -174,8 +196,16 @@ struct MvArgs {
 
 __host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S) {
   // ring, partial sums (two tiles), f16 activations, then counts, slot order, groups
-  return int(kMvWarps * kMvRing * kMvCell + 2 * kMvWarps * 512 + int64_t(group) * K * 2 + (kMvWarps * kMvRing) * 8 +
-             64 + (E + 1) * 8 + S * 8 + 256);
+  return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 + 64 + (E + 1) * 8 + S * 8 + 256);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 template <int kDt>   // kBF16, kFP16, or 2 for fp32
@@ -204,20 +234,28 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16_16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 template <int kDt, bool kGated, int kOut>   // kOut: type of a non-gated result (kBF16, kFP16, 2 = fp32)
 __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs p) {
   extern __shared__ __align__(128) uint8_t mv_smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  uint8_t* ring = mv_smem_raw;                                                    // [warp][slot][cell]
-  float4* red = reinterpret_cast<float4*>(ring + kMvWarps * kMvRing * kMvCell);   // [2][warp][lane]
+  uint8_t* ring = mv_smem_raw;                                                    // [warp][slot]: codes, then scales
+  float4* red = reinterpret_cast<float4*>(ring + kMvWarps * kMvRing * kMvSlot);   // [2][warp][lane]
   uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * kMvWarps * 32);              // f16 [K/32][group][4 quarters][8]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(xs + int64_t(p.group) * p.K * 2);
-  uint32_t* xmax = reinterpret_cast<uint32_t*>(bars + kMvWarps * kMvRing);        // [8] largest magnitude, fp32 bits
+  uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + int64_t(p.group) * p.K * 2);  // [8] largest magnitude, fp32 bits
   int* first = reinterpret_cast<int*>(xmax + 16);                                 // [E + 1] first slot of each expert
   int* gfirst = first + (p.E + 1);                                                // [E + 1] first group
   int* order = gfirst + (p.E + 1);                                                // [S] slots by expert
   int* pos = order + p.S;                                                         // [S] expert and rank among its slots
   __shared__ int wsum[2][kMvWarps];
+  __shared__ uint4 zero;
+  if (tid == 0) zero = make_uint4(0, 0, 0, 0);
 
   // ---- slots grouped by expert, in slot order: every block has to come to the
   // same groups, since the tiles of one group are spread over blocks
@@ -228,8 +266,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     pos[s] = ok ? e : -1;
     if (!ok && blockIdx.x == 0) raise_device_error(9);
   }
-  for (int s = lane; s < kMvRing; s += 32) sm100::mbar_init(sm100::smem_u32(&bars[warp * kMvRing + s]), 1);
-  sm100::fence_mbar_init();
   __syncthreads();
   if (warp == 0) {
     // rank among the expert's slots, 32 slots at a time: those before in the
@@ -244,15 +280,18 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     }
   }
   __syncthreads();
-  {  // exclusive sums over the experts of slots and groups, kMvMaxE / kMvThreads = 2 experts a thread
-    int n[2], gr[2];
+  {  // exclusive sums over the experts of slots and groups, a few experts a thread
+    constexpr int kPer = (kMvMaxE + kMvThreads - 1) / kMvThreads;
+    int n[kPer], gr[kPer], sn = 0, sg = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 2 * tid + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = kPer * tid + i;
       n[i] = e < p.E ? first[e] : 0;
       gr[i] = (n[i] + p.group - 1) / p.group;
+      sn += n[i];
+      sg += gr[i];
     }
-    int sn = n[0] + n[1], sg = gr[0] + gr[1];
+    const int own_n = sn, own_g = sg;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, sn, o), b = __shfl_up_sync(0xffffffffu, sg, o);
@@ -262,11 +301,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     __syncthreads();
     int bn = 0, bg = 0;
     for (int w = 0; w < warp; ++w) { bn += wsum[0][w]; bg += wsum[1][w]; }
-    bn += sn - n[0] - n[1];
-    bg += sg - gr[0] - gr[1];
+    bn += sn - own_n;
+    bg += sg - own_g;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 2 * tid + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = kPer * tid + i;
       if (e < p.E) { first[e] = bn; gfirst[e] = bg; }
       bn += n[i];
       bg += gr[i];
@@ -278,12 +317,18 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     if (pos[s] >= 0) order[first[pos[s] & 1023] + (pos[s] >> 10)] = s;
   __syncthreads();
 
+  // ---- units (group, tile), a contiguous range of them per block, cut into
+  // one segment per group; a segment's units go round the teams of `team_warps`
+  // warps, a unit's cells round the warps of a team
   const int64_t units = int64_t(gfirst[p.E]) * p.tiles;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int cells = p.K >> 7;                                  // 128-column cells of a tile
-  const int mine = warp < cells ? (cells - warp + kMvWarps - 1) / kMvWarps : 0;
-  const int64_t ecodes = p.tiles * cells * 1024, escales = p.tiles * cells * 64;
-  auto expert_of = [&](int64_t grp) {                          // last expert whose first group is at or before grp
+  const int W = p.team_warps, teams = kMvWarps / W;
+  const int team = warp / W, member = warp % W;
+  // this warp's cells of a tile, [cell0, cell0 + mine)
+  const int cell0 = member * cells / W, mine = (member + 1) * cells / W - cell0;
+  const uint32_t ring_at = sm100::smem_u32(ring) + warp * kMvRing * kMvSlot;
+  auto expert_of = [&](int grp) {                              // last expert whose first group is at or before grp
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -291,128 +336,184 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     }
     return lo;
   };
-  // producer side of this warp's ring (lane 0): the next cell to load
-  int64_t lu = u0;
-  int li = 0, ls = 0, le = -1;
-  int64_t lgrp = -1;
-  auto load_next = [&]() {
-    if (mine == 0 || lu >= u1) return;
-    const int64_t grp = lu / p.tiles;
-    if (grp != lgrp) { le = expert_of(grp); lgrp = grp; }
-    const int64_t cell = (lu - grp * p.tiles) * cells + warp + li * kMvWarps;
-    const uint32_t bar = sm100::smem_u32(&bars[warp * kMvRing + ls]);
-    const uint32_t dst = sm100::smem_u32(ring + (warp * kMvRing + ls) * kMvCell);
-    sm100::mbar_arrive_expect_tx(bar, kMvCell);
-    sm100::bulk_load(dst, p.codes + le * ecodes + cell * 1024, 1024, bar);
-    sm100::bulk_load(dst + 1024, p.scales + le * escales + cell * 64, 64, bar);
-    if (++ls == kMvRing) ls = 0;
-    if (++li == mine) { li = 0; ++lu; }
-  };
-  if (lane == 0)
-    for (int i = 0; i < kMvRing; ++i) load_next();
+  const int grp0 = u1 > u0 ? int(u0 / p.tiles) : 0;
+  const int64_t first_tile = u0 - grp0 * p.tiles, total = u1 - u0;
+  // (segment i of this block: group grp0 + i, tiles [tile0, tile1))
 
+  // ---- the warp's next cell to load: `left` units from the start of its
+  // segment on, (ld_grp, ld_tile, ld_i) its place
+  int64_t left = mine > 0 ? total : 0, ld_tile0 = first_tile, ld_tile = 0, ld_tile1 = 0;
+  int ld_grp = grp0, ld_i = 0, ld_slot = 0;
+  const uint8_t *ld_codes = nullptr, *ld_scales = nullptr;
+  const int64_t jump = int64_t(teams) * cells - mine;          // from behind a unit's last cell to the next unit's first
+  auto to_segment = [&]() {                                    // to the team's first unit at or after the segment's start
+    ld_tile = ld_tile0 + team;
+    ld_tile1 = min(p.tiles, ld_tile0 + left);
+    while (ld_tile >= ld_tile1 && left > 0) {
+      left -= ld_tile1 - ld_tile0;
+      ld_tile0 = 0;
+      ++ld_grp;
+      ld_tile = team;
+      ld_tile1 = min(p.tiles, left);
+    }
+    if (left > 0) {
+      const int64_t cell = (expert_of(ld_grp) * p.tiles + ld_tile) * cells + cell0;
+      ld_codes = p.codes + cell * 1024 + lane * 16;
+      ld_scales = p.scales + cell * 64 + (lane & 7) * 16;
+    }
+  };
+  auto load_next = [&]() {
+    if (left > 0) {
+      const uint32_t dst = ring_at + ld_slot * kMvSlot + lane * 16;
+      const int nc = min(kMvCells, mine - ld_i);
+      cp_async16(dst, ld_codes);
+      cp_async16(dst + 512, ld_codes + 512);
+      if (nc > 1) {
+        cp_async16(dst + 1024, ld_codes + 1024);
+        cp_async16(dst + 1536, ld_codes + 1536);
+      }
+      if (lane < 4 * nc) cp_async16(dst + kMvCells * 1024, ld_scales);
+      ld_i += nc;
+      int64_t step = nc;
+      if (ld_i == mine) {
+        ld_i = 0;
+        step += jump;
+        ld_tile += teams;
+      }
+      ld_codes += step * 1024;
+      ld_scales += step * 64;
+      if (ld_tile >= ld_tile1) {                               // on to the next group's segment
+        left -= ld_tile1 - ld_tile0;
+        ld_tile0 = 0;
+        ++ld_grp;
+        to_segment();
+      }
+    }
+    cp_async_commit();                                         // (empty at the end: the waits count groups)
+    if (++ld_slot == kMvRing) ld_slot = 0;
+  };
+  if (left > 0) to_segment();
+  for (int i = 0; i < kMvRing; ++i) load_next();
+
+  int64_t done = 0;                                            // units of the segments before the current one
   int slot = 0;
-  uint32_t phase = 0;
-  bool alive = true;
-  int n = 0, o0 = 0;                                           // slots of the current group and their place in `order`
-  int64_t cur = -1;
-  float xscale[2] = {0.0f, 0.0f};                              // 2^exponent of columns 2q, 2q + 1
-  for (int64_t u = u0; u < u1; ++u) {
-    const int64_t grp = u / p.tiles, tile = u - grp * p.tiles;
-    if (grp != cur) {
-      // ---- this group's activations: row maxima, then f16 into shared memory
-      cur = grp;
-      const int e = expert_of(grp);
-      o0 = first[e] + int(grp - gfirst[e]) * p.group;
-      n = min(p.group, first[e + 1] - o0);
-      __syncthreads();                                         // the previous group's activations are done with
-      if (tid < 8) xmax[tid] = 0;
-      __syncthreads();
-      const int c8 = p.K >> 3;
-      for (int r = 0; r < n; ++r) {
-        const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
-        uint32_t m = 0;
-        for (int c = tid; c < c8; c += kMvThreads) {
-          float f[8];
-          mv_load8<kDt>(p.x, base + 8 * c, f);
+  float4* tred = red + team * 2 * W * 32;                      // this team's partial sums, two units deep
+  for (int grp = grp0; done < total; ++grp) {
+    const int64_t tile0 = grp == grp0 ? first_tile : 0;
+    const int64_t tile1 = min(p.tiles, tile0 + (total - done));
+    done += tile1 - tile0;
+    // ---- this group's activations: row maxima, then f16 into shared memory
+    const int e = expert_of(grp);
+    const int o0 = first[e] + (grp - gfirst[e]) * p.group;     // the group's slots in `order`
+    const int n = min(p.group, first[e + 1] - o0);
+    __syncthreads();                                           // the previous group's activations are done with
+    if (tid < 8) xmax[tid] = 0;
+    __syncthreads();
+    const int c8 = p.K >> 3;
+    for (int r = 0; r < n; ++r) {
+      const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+      uint32_t m = 0;
+      for (int c = tid; c < c8; c += kMvThreads) {
+        float f[8];
+        mv_load8<kDt>(p.x, base + 8 * c, f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
-            if (b < 0x7F800000u) m = max(m, b);                // infinities and NaN stay what they are below
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+          if (b < 0x7F800000u) m = max(m, b);                  // infinities and NaN stay what they are below
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0 && m) atomicMax(&xmax[r], m);
+    }
+    __syncthreads();
+    // power of two that takes the largest magnitude to [2^12, 2^13): exponent field of its inverse
+    auto inv_exp = [&](int r) {
+      const int ef = int(xmax[r] >> 23);
+      return ef == 0 ? 127 : min(254, max(1, 127 + 12 - (ef - 127)));
+    };
+    for (int r = 0; r < n; ++r) {
+      const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+      const float inv = __uint_as_float(uint32_t(inv_exp(r)) << 23);
+      for (int c = tid; c < c8; c += kMvThreads) {
+        float f[8];
+        mv_load8<kDt>(p.x, base + 8 * c, f);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
+        *reinterpret_cast<uint4*>(xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+    float xscale[2];                                           // 2^exponent of columns 2q, 2q + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * q + i;
+      xscale[i] = r < n ? e8m0_to_f32(uint32_t(254 - inv_exp(r))) : 0.0f;
+    }
+    __syncthreads();
+    // this lane's column of a 32-block; columns past the group's slots read one zero piece
+    const uint32_t xlane = g < n ? sm100::smem_u32(xs) + (g * 4 + q) * 16 : sm100::smem_u32(&zero);
+    const int xstep = g < n ? p.group * 64 : 0;
+    int buf = 0;
+    for (int64_t tile = tile0 + team; tile < tile1; tile += teams) {
+      // ---- this warp's cells of the tile
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < mine; i += kMvCells) {
+        // the oldest load has come: into registers, and its slot takes the
+        // next one before the products (a missing second cell: stale bytes,
+        // not used)
+        cp_async_wait<kMvRing - 1>();
+        __syncwarp();
+        const uint32_t at = ring_at + slot * kMvSlot;
+        uint4 wa[kMvCells], wb[kMvCells];
+        uint32_t sa[kMvCells], sb[kMvCells];
+#pragma unroll
+        for (int c = 0; c < kMvCells; ++c) {
+          wa[c] = lds128(at + c * 1024 + lane * 16);
+          wb[c] = lds128(at + c * 1024 + 512 + lane * 16);
+          sa[c] = lds32(at + kMvCells * 1024 + c * 64 + g * 4);
+          sb[c] = lds32(at + kMvCells * 1024 + c * 64 + 32 + g * 4);
+        }
+        __syncwarp();
+        load_next();
+        if (++slot == kMvRing) slot = 0;
+        const uint32_t xb = xlane + (cell0 + i) * 4 * xstep;
+#pragma unroll
+        for (int c = 0; c < kMvCells; ++c) {
+          if (c > 0 && i + c >= mine) break;
+          float fa[4], fb[4];
+          e8m0x4_to_f32(sa[c], fa);
+          e8m0x4_to_f32(sb[c], fb);
+          const uint32_t a[4] = {wa[c].x, wa[c].y, wa[c].z, wa[c].w}, b[4] = {wb[c].x, wb[c].y, wb[c].z, wb[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 xv = lds128(xb + (4 * c + j) * xstep);
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_f16(a[j], ha);
+            e2m1x8_to_f16(b[j], hb);
+            float d[4];
+            mma_f16_16816_zero(d, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
+            mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
+            acc[0] = fmaf(d[0], fa[j], acc[0]);
+            acc[1] = fmaf(d[1], fa[j], acc[1]);
+            acc[2] = fmaf(d[2], fb[j], acc[2]);
+            acc[3] = fmaf(d[3], fb[j], acc[3]);
           }
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0 && m) atomicMax(&xmax[r], m);
       }
-      __syncthreads();
-      // power of two that takes the largest magnitude to [2^12, 2^13): exponent field of its inverse
-      auto inv_exp = [&](int r) { const int ef = int(xmax[r] >> 23); return ef == 0 ? 127 : min(254, max(1, 127 + 12 - (ef - 127))); };
-      for (int r = 0; r < n; ++r) {
-        const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
-        const float inv = __uint_as_float(uint32_t(inv_exp(r)) << 23);
-        for (int c = tid; c < c8; c += kMvThreads) {
-          float f[8];
-          mv_load8<kDt>(p.x, base + 8 * c, f);
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
-          *reinterpret_cast<uint4*>(xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      // ---- one warp of the team adds the partial sums in warp order and
+      // writes the tile; the others go on (the other half of the team's buffer
+      // is theirs until the next barrier)
+      float4 t = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (W > 1) {
+        tred[(buf * W + member) * 32 + lane] = t;
+        sm100::named_bar_sync(1 + team, W * 32);
+        if (member != int(tile) % W) { buf ^= 1; continue; }
+        t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < W; ++w) {
+          const float4 v = tred[(buf * W + w) * 32 + lane];
+          t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * q + i;
-        xscale[i] = r < n ? __uint_as_float(uint32_t(254 - inv_exp(r)) << 23) : 0.0f;
-        if (r < n && inv_exp(r) == 254) xscale[i] = __uint_as_float(0x00400000u);   // 2^-127
-      }
-      __syncthreads();
-    }
-    // ---- this warp's cells of the tile
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < mine; ++i) {
-      const uint32_t bar = sm100::smem_u32(&bars[warp * kMvRing + slot]);
-      if (alive && !sm100::mbar_wait(bar, phase)) alive = false;
-      alive = __all_sync(0xffffffffu, alive);
-      if (alive) {
-        const uint8_t* cell = ring + (warp * kMvRing + slot) * kMvCell;
-        const uint4 wg = *reinterpret_cast<const uint4*>(cell + lane * 16);
-        const uint4 wu = *reinterpret_cast<const uint4*>(cell + 512 + lane * 16);
-        const uint32_t sg = *reinterpret_cast<const uint32_t*>(cell + 1024 + g * 4);
-        const uint32_t su = *reinterpret_cast<const uint32_t*>(cell + 1024 + 32 + g * 4);
-        __syncwarp();
-        if (lane == 0) load_next();
-        const int kb = (warp + i * kMvWarps) * 4;              // first 32-block of the cell
-        const uint32_t a[4] = {wg.x, wg.y, wg.z, wg.w}, b[4] = {wu.x, wu.y, wu.z, wu.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 xv = make_uint4(0, 0, 0, 0);
-          if (g < n) xv = *reinterpret_cast<const uint4*>(xs + ((int64_t(kb + j) * p.group + g) * 4 + q) * 16);
-          uint32_t ha[4], hb[4];
-          e2m1x8_to_f16(a[j], ha);
-          e2m1x8_to_f16(b[j], hb);
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_f16_16816(c, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
-          mma_f16_16816(c, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
-          const float s0 = e8m0_to_f32((sg >> (8 * j)) & 0xFFu), s1 = e8m0_to_f32((su >> (8 * j)) & 0xFFu);
-          acc[0] = fmaf(c[0], s0, acc[0]);
-          acc[1] = fmaf(c[1], s0, acc[1]);
-          acc[2] = fmaf(c[2], s1, acc[2]);
-          acc[3] = fmaf(c[3], s1, acc[3]);
-        }
-      }
-      if (++slot == kMvRing) { slot = 0; phase ^= 1; }
-    }
-    const int buf = int(u & 1);
-    red[(buf * kMvWarps + warp) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    // ---- one warp adds the partial sums in warp order and writes the tile;
-    // the others go on (the other half of `red` is theirs until the next barrier)
-    if (warp == int(tile % kMvWarps)) {
-      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kMvWarps; ++w) {
-        const float4 v = red[(buf * kMvWarps + w) * 32 + lane];
-        t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+        buf ^= 1;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -435,7 +536,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       }
     }
   }
-  if (!alive && lane == 0) raise_device_error(7);
 }
 
 // out[t] = sum_j w[t, j] y[t * k + j] in fp32, j order, rounded once; a slot

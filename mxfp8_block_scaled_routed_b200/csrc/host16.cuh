@@ -87,6 +87,9 @@ int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream) {
   MX_TRY(ensure_smem(kern, done, 232448 - 1024));
   a.group = mv_group(a.K, a.E, a.S);
   if (a.group == 0) return fail(MXMOE_ERR_SHAPE, "K=%d with E=%d and %d slots does not fit shared memory", a.K, a.E, a.S);
+  // as many warps share a tile as leave each four cells or more of it
+  a.team_warps = kMvWarps & -kMvWarps;
+  while (a.team_warps > 1 && a.team_warps * 4 > a.K / 128) a.team_warps >>= 1;
   const int grid = int(std::min<int64_t>(int64_t(a.S) * a.tiles, d->sms));
   kern<<<grid, kMvThreads, mv_smem(a.K, a.group, a.E, a.S), stream>>>(a);
   MX_CHECK_CUDA(cudaGetLastError(), "4-bit matvec launch");
