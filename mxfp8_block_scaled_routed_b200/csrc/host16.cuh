@@ -47,8 +47,21 @@ int launch_ragged_dt(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
   static std::atomic<uint64_t> done{0};
   auto kern = ragged::ragged_gemm_kernel<kMode, kDt>;
   MX_TRY(ensure_smem(kern, done, ragged::Cfg::SMEM_BYTES));
-  const int grid = int(std::min<int64_t>(max_tiles, d->sms));
-  kern<<<grid, 384, ragged::Cfg::SMEM_BYTES, stream>>>(ma, mb, mo, p);
+  if (max_tiles > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "%lld tiles: too large", (long long)max_tiles);
+  // clusters of two CTAs, as many as can be resident
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(384, 1, 1);
+  cfg.dynamicSmemBytes = ragged::Cfg::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(max_tiles, d->sms / 2)), 1, 1);
+  MX_CHECK_CUDA(cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, p), "ragged product launch");
   MX_CHECK_CUDA(cudaGetLastError(), "ragged product launch");
   return MXMOE_OK;
 }
@@ -160,7 +173,7 @@ int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N,
   p.kext = int(transpose_w ? N : K);
   CUtensorMap ma, mb;
   MX_TRY(make_map16(&ma, dtype, w, 3, K, N, E, 64, transpose_w ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B, "weights"));
-  MX_TRY(make_map16(&mb, dtype, a, 2, p.kext, M, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
+  MX_TRY(make_map16(&mb, dtype, a, 2, p.kext, M, 1, 64, ragged::Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
   // every segment's last tile may be short
   const int64_t tiles = (M / ragged::Cfg::BN + std::min<int64_t>(E, M)) * ((p.rows + ragged::Cfg::BM - 1) / ragged::Cfg::BM);
   return transpose_w ? launch_ragged<ragged::kDgrad>(dtype, ma, mb, mb, p, tiles, d, stream)
