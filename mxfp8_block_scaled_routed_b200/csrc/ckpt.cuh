@@ -77,88 +77,114 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack16x2<kDt>(x[6], x[7]));
 }
 
-// Row and unit of this thread; false past the last row.
-__device__ __forceinline__ bool ckpt_place(const CkptArgs& p, int64_t& row, uint32_t& unit) {
-  const int64_t first = int64_t(blockIdx.x) * 256;
-  const int64_t r0 = first / p.units;
-  const uint32_t u = uint32_t(first - r0 * p.units) + threadIdx.x;
-  const uint32_t dr = u / p.units;
+// Row and unit of this thread's i-th unit (kCkptUnits of them, a block's width
+// apart); false past the last row or the last column.
+constexpr int kCkptUnits = 2;
+
+__device__ __forceinline__ bool ckpt_place(const CkptArgs& p, int64_t r0, uint32_t u0, int64_t limit, int i, int64_t& row,
+                                           uint32_t& unit) {
+  const uint32_t u = u0 + i * 256 + threadIdx.x, dr = u / p.units;
   row = r0 + dr;
   unit = u - dr * p.units;
-  int64_t limit = p.rows;
-  if (p.rows_dev) limit = min(limit, int64_t(*p.rows_dev));
-  return row < limit;
+  return row < limit && unit * 8 < p.F;
+}
+
+__device__ __forceinline__ uint32_t ckpt_byte(uint32_t m) {
+  if (m >= 0x7F800000u) return 0xFFu;
+  const int e = int(m >> 23) - 8;
+  return uint32_t(e < 0 ? 0 : e);
 }
 
 template <int kDt>
 __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const CkptArgs p) {
-  int64_t row;
-  uint32_t unit;
-  const bool live = ckpt_place(p, row, unit) && unit * 8 < p.F;
-  const uint32_t c = unit * 8;
-  uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-  if (live) {
-    const uint16_t* src = p.in + row * 2 * p.F + c;
-    va = __ldcs(reinterpret_cast<const uint4*>(src));
-    vb = __ldcs(reinterpret_cast<const uint4*>(src + p.F));
-  }
-  uint32_t ma = absmax_f32bits8<kDt>(va), mb = absmax_f32bits8<kDt>(vb);
+  const int64_t first = int64_t(blockIdx.x) * (256 * kCkptUnits), r0 = first / p.units;
+  const uint32_t u0 = uint32_t(first - r0 * p.units);
+  const int64_t limit = p.rows_dev ? min(p.rows, int64_t(*p.rows_dev)) : p.rows;
+  uint4 va[kCkptUnits], vb[kCkptUnits];
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+  for (int i = 0; i < kCkptUnits; ++i) {
+    int64_t row;
+    uint32_t unit;
+    va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+    if (ckpt_place(p, r0, u0, limit, i, row, unit)) {
+      const uint16_t* src = p.in + row * 2 * p.F + unit * 8;
+      va[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+      vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + p.F));
+    }
   }
-  if (!live) return;
-  auto byte_of = [](uint32_t m) {
-    if (m >= 0x7F800000u) return 0xFFu;
-    const int e = int(m >> 23) - 8;
-    return uint32_t(e < 0 ? 0 : e);
-  };
-  const uint32_t ba = byte_of(ma), bb = byte_of(mb);
-  float a[8], b[8], h[8];
-  unpack8<kDt>(va, a);
-  unpack8<kDt>(vb, b);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = silu_mul(a[i], b[i]);
-  uint8_t* codes = p.codes + row * 2 * p.F + c;
-  *reinterpret_cast<uint2*>(codes) = e4m3_encode8(a, ba);
-  *reinterpret_cast<uint2*>(codes + p.F) = e4m3_encode8(b, bb);
-  *reinterpret_cast<uint4*>(p.h + row * p.F + c) = pack8<kDt>(h);
-  if ((unit & 3) == 0) {
-    const uint32_t nb = p.units >> 2;
-    uint8_t* s = p.scales + row * 2 * nb + (unit >> 2);
-    s[0] = uint8_t(ba);
-    s[nb] = uint8_t(bb);
+  for (int i = 0; i < kCkptUnits; ++i) {
+    uint32_t ma = absmax_f32bits8<kDt>(va[i]), mb = absmax_f32bits8<kDt>(vb[i]);
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    int64_t row;
+    uint32_t unit;
+    if (!ckpt_place(p, r0, u0, limit, i, row, unit)) continue;
+    const uint32_t ba = ckpt_byte(ma), bb = ckpt_byte(mb), c = unit * 8;
+    float a[8], b[8], h[8];
+    unpack8<kDt>(va[i], a);
+    unpack8<kDt>(vb[i], b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = silu_mul(a[j], b[j]);
+    uint8_t* codes = p.codes + row * 2 * p.F + c;
+    *reinterpret_cast<uint2*>(codes) = e4m3_encode8(a, ba);
+    *reinterpret_cast<uint2*>(codes + p.F) = e4m3_encode8(b, bb);
+    *reinterpret_cast<uint4*>(p.h + row * p.F + c) = pack8<kDt>(h);
+    if ((unit & 3) == 0) {
+      const uint32_t nb = p.units >> 2;
+      uint8_t* s = p.scales + row * 2 * nb + (unit >> 2);
+      s[0] = uint8_t(ba);
+      s[nb] = uint8_t(bb);
+    }
   }
 }
 
 template <int kDt>
 __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const CkptArgs p) {
-  int64_t row;
-  uint32_t unit;
-  if (!ckpt_place(p, row, unit) || unit * 8 >= p.F) return;
-  const uint32_t c = unit * 8, nb = p.units >> 2;
-  const uint8_t* codes = p.codes + row * 2 * p.F + c;
-  const uint8_t* sc = p.scales + row * 2 * nb + (unit >> 2);
-  const uint4 vd = __ldcs(reinterpret_cast<const uint4*>(p.in + row * p.F + c));
-  const uint2 ca = __ldcs(reinterpret_cast<const uint2*>(codes));
-  const uint2 cb = __ldcs(reinterpret_cast<const uint2*>(codes + p.F));
-  const float sa = e8m0_to_f32(sc[0]), sb = e8m0_to_f32(sc[nb]);
-  float a[8], b[8], d[8], da[8], db[8], h[8];
-  e4m3_decode8(ca, sa, a);
-  e4m3_decode8(cb, sb, b);
-  unpack8<kDt>(vd, d);
+  const int64_t first = int64_t(blockIdx.x) * (256 * kCkptUnits), r0 = first / p.units;
+  const uint32_t u0 = uint32_t(first - r0 * p.units), nb = p.units >> 2;
+  const int64_t limit = p.rows_dev ? min(p.rows, int64_t(*p.rows_dev)) : p.rows;
+  uint4 vd[kCkptUnits];
+  uint2 ca[kCkptUnits], cb[kCkptUnits];
+  uint32_t sa[kCkptUnits], sb[kCkptUnits];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = sigmoid_fast(a[i]);
-    da[i] = d[i] * b[i] * s * (1.0f + a[i] * (1.0f - s));
-    db[i] = d[i] * a[i] * s;
-    h[i] = a[i] * s * b[i];
+  for (int i = 0; i < kCkptUnits; ++i) {
+    int64_t row;
+    uint32_t unit;
+    if (!ckpt_place(p, r0, u0, limit, i, row, unit)) continue;
+    const uint8_t* codes = p.codes + row * 2 * p.F + unit * 8;
+    const uint8_t* sc = p.scales + row * 2 * nb + (unit >> 2);
+    vd[i] = __ldcs(reinterpret_cast<const uint4*>(p.in + row * p.F + unit * 8));
+    ca[i] = __ldcs(reinterpret_cast<const uint2*>(codes));
+    cb[i] = __ldcs(reinterpret_cast<const uint2*>(codes + p.F));
+    sa[i] = sc[0];
+    sb[i] = sc[nb];
   }
-  uint16_t* g = p.dh13 + row * 2 * p.F + c;
-  *reinterpret_cast<uint4*>(g) = pack8<kDt>(da);
-  *reinterpret_cast<uint4*>(g + p.F) = pack8<kDt>(db);
-  if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.F + c) = pack8<kDt>(h);
+#pragma unroll
+  for (int i = 0; i < kCkptUnits; ++i) {
+    int64_t row;
+    uint32_t unit;
+    if (!ckpt_place(p, r0, u0, limit, i, row, unit)) continue;
+    const uint32_t c = unit * 8;
+    float a[8], b[8], d[8], da[8], db[8], h[8];
+    e4m3_decode8(ca[i], e8m0_to_f32(sa[i]), a);
+    e4m3_decode8(cb[i], e8m0_to_f32(sb[i]), b);
+    unpack8<kDt>(vd[i], d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = sigmoid_fast(a[j]);
+      da[j] = d[j] * b[j] * s * (1.0f + a[j] * (1.0f - s));
+      db[j] = d[j] * a[j] * s;
+      h[j] = a[j] * s * b[j];
+    }
+    uint16_t* g = p.dh13 + row * 2 * p.F + c;
+    *reinterpret_cast<uint4*>(g) = pack8<kDt>(da);
+    *reinterpret_cast<uint4*>(g + p.F) = pack8<kDt>(db);
+    if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.F + c) = pack8<kDt>(h);
+  }
 }
 
 }  // namespace mxmoe

@@ -60,15 +60,10 @@ __device__ __forceinline__ void e8m0x4_to_f32(uint32_t w, float (&f)[4]) {
   f[3] = bf16hi_to_f32(hi);
 }
 
-// Byte offset of the codes (and of the scale) of row r, columns 8 c8.. in one
-// expert's matrix of R rows and K columns.
+// Byte offset of the codes (and of the scale) of row r, columns 8 c8.. in the
+// tile layout of one expert's matrix of R rows and K columns.
 __device__ __forceinline__ void fp4_place(int layout, int64_t r, uint32_t c8, int64_t R, int64_t K, int64_t& code,
                                           int64_t& scale) {
-  if (layout == kFp4Plain) {
-    code = r * (K >> 1) + 4 * int64_t(c8);
-    scale = r * (K >> 5) + (c8 >> 2);
-    return;
-  }
   int64_t t = r >> 4;
   uint32_t row = uint32_t(r & 15);
   if (layout == kFp4TileGated) {
@@ -84,67 +79,94 @@ __device__ __forceinline__ void fp4_place(int layout, int64_t r, uint32_t c8, in
   scale = cell * 64 + row * 4 + j;
 }
 
-// One thread per eight columns, a 32-block on four neighbouring lanes.  Bound
-// by HBM: 2 + 17/32 bytes a value.
+// Eight columns a unit, a 32-block on four neighbouring lanes, kFp4Units units
+// a thread (a block's width apart) with their loads issued first.  Bound by
+// HBM: 2 + 17/32 bytes a value either way.
+constexpr int kFp4Units = 4;
+
 template <int kDt>
 __global__ void __launch_bounds__(256)
 fp4_quantize_kernel(const uint16_t* __restrict__ x, int64_t batch, int64_t R, int64_t K, int layout,
                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const uint32_t upr = uint32_t(K >> 3);                      // eight-column units per row, a multiple of 4
-  const int64_t first = int64_t(blockIdx.x) * 256;
-  const int64_t r0 = first / upr;
-  const uint32_t u = uint32_t(first - r0 * upr) + threadIdx.x;
-  const uint32_t dr = u / upr;
-  const int64_t row = r0 + dr;                                // of the [batch * R, K] matrix
-  const uint32_t c8 = u - dr * upr;
-  const bool live = row < batch * R;                          // whole 32-blocks: uniform in each group of four lanes
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (live) v = __ldcs(reinterpret_cast<const uint4*>(x + row * K) + c8);
-  uint32_t m = absmax_f32bits8<kDt>(v);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (!live) return;
-  uint32_t byte = 0xFFu, w = 0;
-  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-  if (m < 0x7F800000u) {
-    const int e = int(m >> 23) - 2;
-    byte = uint32_t(e < 0 ? 0 : e);
-    const float inv = inv_scale_from_byte(byte);
+  const uint32_t upr = uint32_t(K >> 3);                      // units per row, a multiple of 4
+  const int64_t first = int64_t(blockIdx.x) * (256 * kFp4Units), total = batch * R * upr;
+  uint4 v[kFp4Units];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack16x2<kDt>(in[i]);
-      w |= e2m1x2(f.x * inv, f.y * inv) << (8 * i);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)                               // magnitude 6 and the sign; the byte makes it NaN
-      w |= (0x77u | ((in[i] >> 12) & 8u) | ((in[i] >> 24) & 0x80u)) << (8 * i);
+  for (int i = 0; i < kFp4Units; ++i) {
+    const int64_t u = first + i * 256 + threadIdx.x;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (u < total) v[i] = __ldcs(reinterpret_cast<const uint4*>(x) + u);
   }
-  const int64_t e = layout == kFp4Plain ? 0 : row / R;
-  int64_t oc, os;
-  fp4_place(layout, row - e * R, c8, R, K, oc, os);
-  *reinterpret_cast<uint32_t*>(codes + e * R * (K >> 1) + oc) = w;
-  if ((c8 & 3) == 0) scales[e * R * (K >> 5) + os] = uint8_t(byte);
+  const int64_t r0 = first / upr;                             // row of the [batch * R, K] matrix
+  const uint32_t c0 = uint32_t(first - r0 * upr);
+#pragma unroll
+  for (int i = 0; i < kFp4Units; ++i) {
+    uint32_t m = absmax_f32bits8<kDt>(v[i]);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int64_t u = first + i * 256 + threadIdx.x;
+    if (u >= total) continue;                                 // whole 32-blocks: uniform in each group of four lanes
+    uint32_t byte = 0xFFu, w = 0;
+    const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    if (m < 0x7F800000u) {
+      const int e = int(m >> 23) - 2;
+      byte = uint32_t(e < 0 ? 0 : e);
+      const float inv = inv_scale_from_byte(byte);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack16x2<kDt>(in[j]);
+        w |= e2m1x2(f.x * inv, f.y * inv) << (8 * j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)                             // magnitude 6 and the sign; the byte makes it NaN
+        w |= (0x77u | ((in[j] >> 12) & 8u) | ((in[j] >> 24) & 0x80u)) << (8 * j);
+    }
+    if (layout == kFp4Plain) {
+      reinterpret_cast<uint32_t*>(codes)[u] = w;
+      if ((u & 3) == 0) scales[u >> 2] = uint8_t(byte);
+    } else {
+      const uint32_t at = c0 + i * 256 + threadIdx.x, dr = at / upr, c8 = at - dr * upr;
+      const int64_t row = r0 + dr, e = row / R;
+      int64_t oc, os;
+      fp4_place(layout, row - e * R, c8, R, K, oc, os);
+      *reinterpret_cast<uint32_t*>(codes + e * R * (K >> 1) + oc) = w;
+      if ((c8 & 3) == 0) scales[e * R * (K >> 5) + os] = uint8_t(byte);
+    }
+  }
 }
 
-// PLAIN -> 16-bit values, one thread per eight columns: code * 2^(byte - 127)
-// is exact in fp32 and rounded once (bf16: never, but below 2^-133).
+// PLAIN -> 16-bit values: code * 2^(byte - 127) is exact in fp32 and rounded
+// once (bf16: never, but below 2^-133).
 template <int kDt>
 __global__ void __launch_bounds__(256)
 fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t units,
                       uint4* __restrict__ out) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= units) return;
-  const uint32_t w = __ldcs(codes + i);
-  const float s = e8m0_to_f32(scales[i >> 2]);
-  uint32_t h[4], o[4];
-  e2m1x8_to_f16(w, h);
+  const int64_t first = int64_t(blockIdx.x) * (256 * kFp4Units) + threadIdx.x;
+  uint32_t w[kFp4Units], b[kFp4Units];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-    o[j] = pack16x2<kDt>(f.x * s, f.y * s);
+  for (int i = 0; i < kFp4Units; ++i) {
+    const int64_t u = first + i * 256;
+    w[i] = b[i] = 0;
+    if (u < units) {
+      w[i] = __ldcs(codes + u);
+      b[i] = scales[u >> 2];
+    }
   }
-  out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+  for (int i = 0; i < kFp4Units; ++i) {
+    const int64_t u = first + i * 256;
+    if (u >= units) continue;
+    const float s = e8m0_to_f32(b[i]);
+    uint32_t h[4], o[4];
+    e2m1x8_to_f16(w[i], h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      o[j] = pack16x2<kDt>(f.x * s, f.y * s);
+    }
+    __stcs(out + u, make_uint4(o[0], o[1], o[2], o[3]));
+  }
 }
 
 // ---------------------------------------------------------------- matvec

@@ -125,7 +125,7 @@ int ckpt_args(CkptArgs* a, int64_t rows, int64_t F, const int32_t* rows_dev, int
   a->F = uint32_t(F);
   a->units = uint32_t((F + 31) / 32 * 4);
   if (rows > (int64_t(1) << 62) / a->units) return fail(MXMOE_ERR_SHAPE, "rows=%lld too large", (long long)rows);
-  *blocks = (rows * a->units + 255) / 256;
+  *blocks = (rows * a->units + 256 * kCkptUnits - 1) / (256 * kCkptUnits);
   if (*blocks > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "rows=%lld x F=%lld: too large", (long long)rows, (long long)F);
   return MXMOE_OK;
 }
@@ -257,7 +257,8 @@ int mxfp4_quantize(const void* x, int64_t batch, int64_t rows, int64_t cols, int
   MX_TRY(check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales}}));
   DevInfo* d;
   MX_TRY(device_info(&d));
-  const unsigned blocks = unsigned((batch * rows * (cols / 8) + 255) / 256);
+  const int64_t per = 256 * kFp4Units;
+  const unsigned blocks = unsigned((batch * rows * (cols / 8) + per - 1) / per);
   const auto* in = static_cast<const uint16_t*>(x);
   if (dtype == MXMOE_BF16) fp4_quantize_kernel<kBF16><<<blocks, 256, 0, stream>>>(in, batch, rows, cols, layout, codes, scales);
   else fp4_quantize_kernel<kFP16><<<blocks, 256, 0, stream>>>(in, batch, rows, cols, layout, codes, scales);
@@ -273,7 +274,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
   DevInfo* d;
   MX_TRY(device_info(&d));
   const int64_t units = rows * (cols / 8);
-  const unsigned blocks = unsigned((units + 255) / 256);
+  const int64_t per = 256 * kFp4Units;
+  const unsigned blocks = unsigned((units + per - 1) / per);
   const auto* c = reinterpret_cast<const uint32_t*>(codes);
   auto* o = static_cast<uint4*>(out);
   if (dtype == MXMOE_BF16) fp4_dequantize_kernel<kBF16><<<blocks, 256, 0, stream>>>(c, scales, units, o);
