@@ -9,6 +9,7 @@ unbuilt library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -632,6 +633,8 @@ def _like(t, ref, shape, dtype, name: str):
     """t checked against a shape, a type and ref's device; None allocates it there."""
     if t is None:
         return ref.new_empty(shape, dtype=dtype)
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == ref.device and t.is_contiguous():
+        return t                                       # (ref is a CUDA tensor; below: which of these it was)
     _need(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -789,12 +792,17 @@ def mxfp4_quantize_experts(w13, w2):
     return dict(w13_codes=a["codes"], w13_scales=a["scales"], w2_codes=b["codes"], w2_scales=b["scales"])
 
 
+@functools.lru_cache(maxsize=256)
+def decode_workspace_bytes(T, top_k, D, F):
+    return int(lib().mxfp4_decode_workspace_size(T, top_k, D, F))
+
+
 def moe_layer_decode_fp4(x_tokens, topk_ids, topk_weights, qw, out=None, workspace=None):
     """Routed-experts layer on 4-bit weights for one to a few tokens (T * top_k <= 2048).
 
     x_tokens [T, D] bf16 or fp16, topk_ids int32 and topk_weights fp32 [T, top_k], qw from mxfp4_quantize_experts:
     out[t] = sum_j topk_weights[t, j] * W2[e] . (silu(gate) * up), [gate | up] = W13[e] . x[t], e = topk_ids[t, j].
-    workspace (optional): uint8, at least mxfp4_decode_workspace_size bytes; calls that may overlap need one each."""
+    workspace (optional): uint8, at least decode_workspace_bytes(T, top_k, D, F) long; calls that may overlap need one each."""
     dt = _dtype(x_tokens, "x_tokens")
     if x_tokens.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("x_tokens must be [T, D] and topk_ids [T, top_k]")
@@ -810,7 +818,7 @@ def moe_layer_decode_fp4(x_tokens, topk_ids, topk_weights, qw, out=None, workspa
     _like(qw["w2_scales"], x_tokens, (E, D, F // 32), torch.uint8, "qw['w2_scales']")
     out = _like(out, x_tokens, (T, D), x_tokens.dtype, "out")
     if workspace is None:
-        workspace = _u8((lib().mxfp4_decode_workspace_size(T, k, D, F),), x_tokens.device)
+        workspace = x_tokens.new_empty((decode_workspace_bytes(T, k, D, F),), dtype=torch.uint8)
     else:
         _like(workspace, x_tokens, workspace.shape, torch.uint8, "workspace")
     st = _Q4Weights(c13.data_ptr(), qw["w13_scales"].data_ptr(), c2.data_ptr(), qw["w2_scales"].data_ptr())

@@ -218,8 +218,13 @@ struct MvArgs {
 
 __host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S) {
   // ring, partial sums (two tiles), f16 activations, then counts, slot order, groups
-  return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 + 64 + (E + 1) * 8 + S * 8 + 256);
+  return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 + 64 + (E + 1) * 4 + (4 * S + 1) * 4 + 256);
 }
+
+// Programmatic dependent launch: the next launch of the stream may start its
+// blocks as this grid's leave; it waits for all of this grid's results itself.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -271,78 +276,115 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   float4* red = reinterpret_cast<float4*>(ring + kMvWarps * kMvRing * kMvSlot);   // [2][warp][lane]
   uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * kMvWarps * 32);              // f16 [K/32][group][4 quarters][8]
   uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + int64_t(p.group) * p.K * 2);  // [8] largest magnitude, fp32 bits
-  int* first = reinterpret_cast<int*>(xmax + 16);                                 // [E + 1] first slot of each expert
-  int* gfirst = first + (p.E + 1);                                                // [E + 1] first group
-  int* order = gfirst + (p.E + 1);                                                // [S] slots by expert
-  int* pos = order + p.S;                                                         // [S] expert and rank among its slots
+  int* order = reinterpret_cast<int*>(xmax + 16);                                 // [S] slots, group after group
+  int* gexp = order + p.S;                                                        // [S] expert of each group
+  int* gstart = gexp + p.S;                                                       // [S + 1] its first place in `order`
+  int* pos = gstart + (p.S + 1);                                                  // [S] expert and rank among its slots
+  int* first = pos + p.S;                                                         // [E + 1] first slot of each expert
   __shared__ int wsum[2][kMvWarps];
   __shared__ uint4 zero;
   if (tid == 0) zero = make_uint4(0, 0, 0, 0);
+  launch_dependents();
 
   // ---- slots grouped by expert, in slot order: every block has to come to the
   // same groups, since the tiles of one group are spread over blocks
-  for (int e = tid; e <= p.E; e += kMvThreads) first[e] = 0;
-  for (int s = tid; s < p.S; s += kMvThreads) {
-    const int e = p.ids[s];
-    const bool ok = e >= 0 && e < p.E;
-    pos[s] = ok ? e : -1;
-    if (!ok && blockIdx.x == 0) raise_device_error(9);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // rank among the expert's slots, 32 slots at a time: those before in the
-    // batch and those of the batches before (expert in the low ten bits of pos)
-    for (int b = 0; b < p.S; b += 32) {
-      const int e = b + lane < p.S ? pos[b + lane] : -1;
-      const unsigned peers = __match_any_sync(0xffffffffu, e);
-      if (e >= 0) pos[b + lane] = e | ((first[e] + __popc(peers & ((1u << lane) - 1u))) << 10);
-      __syncwarp();
-      if (e >= 0 && lane == __ffs(peers) - 1) first[e] += __popc(peers);
-      __syncwarp();
-    }
-  }
-  __syncthreads();
-  {  // exclusive sums over the experts of slots and groups, a few experts a thread
-    constexpr int kPer = (kMvMaxE + kMvThreads - 1) / kMvThreads;
-    int n[kPer], gr[kPer], sn = 0, sg = 0;
+  __shared__ int ngroups;
+  if (p.S <= 32) {
+    // one warp, no counters: a group starts at every slot whose rank among its
+    // expert's slots is a multiple of the group size
+    if (warp == 0) {
+      int e = lane < p.S ? p.ids[lane] : -1;
+      if (lane < p.S && (e < 0 || e >= p.E)) {
+        e = -1;
+        if (blockIdx.x == 0) raise_device_error(9);
+      }
+      const unsigned peers = __match_any_sync(0xffffffffu, e), lt = (1u << lane) - 1u;
+      const int rank = __popc(peers & lt), part = rank / p.group, in = rank - part * p.group;
+      const unsigned heads = __ballot_sync(0xffffffffu, e >= 0 && in == 0);
+      const int g0 = __popc(heads & lt);                       // of a head: its group
+      const int size = min(p.group, __popc(peers) - rank);     // of a head: its slots
+      int at = e >= 0 && in == 0 ? size : 0;                   // exclusive sum over the heads
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = kPer * tid + i;
-      n[i] = e < p.E ? first[e] : 0;
-      gr[i] = (n[i] + p.group - 1) / p.group;
-      sn += n[i];
-      sg += gr[i];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      at -= e >= 0 && in == 0 ? size : 0;
+      // a member's head: the slot of its expert with rank part * group
+      unsigned rest = peers;
+      for (int i = 0; i < part * p.group; ++i) rest &= rest - 1;
+      const int base = __shfl_sync(0xffffffffu, at, __ffs(rest) - 1);
+      if (e >= 0) {
+        order[base + in] = lane;
+        if (in == 0) { gexp[g0] = e; gstart[g0] = at; }
+      }
+      const int live = __popc(__ballot_sync(0xffffffffu, e >= 0));
+      if (lane == 0) { ngroups = __popc(heads); gstart[__popc(heads)] = live; }
     }
-    const int own_n = sn, own_g = sg;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, sn, o), b = __shfl_up_sync(0xffffffffu, sg, o);
-      if (lane >= o) { sn += a; sg += b; }
-    }
-    if (lane == 31) { wsum[0][warp] = sn; wsum[1][warp] = sg; }
     __syncthreads();
-    int bn = 0, bg = 0;
-    for (int w = 0; w < warp; ++w) { bn += wsum[0][w]; bg += wsum[1][w]; }
-    bn += sn - own_n;
-    bg += sg - own_g;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = kPer * tid + i;
-      if (e < p.E) { first[e] = bn; gfirst[e] = bg; }
-      bn += n[i];
-      bg += gr[i];
+  } else {
+    for (int e = tid; e <= p.E; e += kMvThreads) first[e] = 0;
+    for (int s = tid; s < p.S; s += kMvThreads) {
+      const int e = p.ids[s];
+      const bool ok = e >= 0 && e < p.E;
+      pos[s] = ok ? e : -1;
+      if (!ok && blockIdx.x == 0) raise_device_error(9);
     }
-    if (tid == kMvThreads - 1) { first[p.E] = bn; gfirst[p.E] = bg; }   // the totals, E = 1024 included
+    __syncthreads();
+    if (warp == 0) {
+      // rank among the expert's slots, 32 slots at a time: those before in the
+      // batch and those of the batches before (expert in the low ten bits of pos)
+      for (int b = 0; b < p.S; b += 32) {
+        const int e = b + lane < p.S ? pos[b + lane] : -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        if (e >= 0) pos[b + lane] = e | ((first[e] + __popc(peers & ((1u << lane) - 1u))) << 10);
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(peers) - 1) first[e] += __popc(peers);
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    {  // exclusive sums over the experts of slots and groups, a few experts a thread
+      constexpr int kPer = (kMvMaxE + kMvThreads - 1) / kMvThreads;
+      int n[kPer], sn = 0, sg = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = kPer * tid + i;
+        n[i] = e < p.E ? first[e] : 0;
+        sn += n[i];
+        sg += (n[i] + p.group - 1) / p.group;
+      }
+      const int own_n = sn, own_g = sg;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, sn, o), b = __shfl_up_sync(0xffffffffu, sg, o);
+        if (lane >= o) { sn += a; sg += b; }
+      }
+      if (lane == 31) { wsum[0][warp] = sn; wsum[1][warp] = sg; }
+      __syncthreads();
+      int bn = 0, bg = 0;
+      for (int w = 0; w < warp; ++w) { bn += wsum[0][w]; bg += wsum[1][w]; }
+      bn += sn - own_n;
+      bg += sg - own_g;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = kPer * tid + i;
+        if (e < p.E) first[e] = bn;
+        for (int o = 0; o < n[i]; o += p.group) { gexp[bg] = e; gstart[bg++] = bn + o; }
+        bn += n[i];
+      }
+      if (tid == kMvThreads - 1) { ngroups = bg; gstart[bg] = bn; }
+    }
+    __syncthreads();
+    for (int s = tid; s < p.S; s += kMvThreads)
+      if (pos[s] >= 0) order[first[pos[s] & 1023] + (pos[s] >> 10)] = s;
+    __syncthreads();
   }
-  __syncthreads();
-  for (int s = tid; s < p.S; s += kMvThreads)
-    if (pos[s] >= 0) order[first[pos[s] & 1023] + (pos[s] >> 10)] = s;
-  __syncthreads();
 
   // ---- units (group, tile), a contiguous range of them per block, cut into
   // one segment per group; a segment's units go round the teams of `team_warps`
   // warps, a unit's cells round the warps of a team
-  const int64_t units = int64_t(gfirst[p.E]) * p.tiles;
+  const int64_t units = int64_t(ngroups) * p.tiles;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int cells = p.K >> 7;                                  // 128-column cells of a tile
   const int W = p.team_warps, teams = kMvWarps / W;
@@ -350,14 +392,6 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   // this warp's cells of a tile, [cell0, cell0 + mine)
   const int cell0 = member * cells / W, mine = (member + 1) * cells / W - cell0;
   const uint32_t ring_at = sm100::smem_u32(ring) + warp * kMvRing * kMvSlot;
-  auto expert_of = [&](int grp) {                              // last expert whose first group is at or before grp
-    int lo = 0, hi = p.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (gfirst[mid] <= grp) lo = mid; else hi = mid;
-    }
-    return lo;
-  };
   const int grp0 = u1 > u0 ? int(u0 / p.tiles) : 0;
   const int64_t first_tile = u0 - grp0 * p.tiles, total = u1 - u0;
   // (segment i of this block: group grp0 + i, tiles [tile0, tile1))
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       ld_tile1 = min(p.tiles, left);
     }
     if (left > 0) {
-      const int64_t cell = (expert_of(ld_grp) * p.tiles + ld_tile) * cells + cell0;
+      const int64_t cell = (gexp[ld_grp] * p.tiles + ld_tile) * cells + cell0;
       ld_codes = p.codes + cell * 1024 + lane * 16;
       ld_scales = p.scales + cell * 64 + (lane & 7) * 16;
     }
@@ -416,6 +450,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   };
   if (left > 0) to_segment();
   for (int i = 0; i < kMvRing; ++i) load_next();
+  // up to here only the ids and the weights were read; x may be the result of
+  // the launch before this one
+  wait_dependency();
 
   int64_t done = 0;                                            // units of the segments before the current one
   int slot = 0;
@@ -425,44 +462,74 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     const int64_t tile1 = min(p.tiles, tile0 + (total - done));
     done += tile1 - tile0;
     // ---- this group's activations: row maxima, then f16 into shared memory
-    const int e = expert_of(grp);
-    const int o0 = first[e] + (grp - gfirst[e]) * p.group;     // the group's slots in `order`
-    const int n = min(p.group, first[e + 1] - o0);
+    const int o0 = gstart[grp], n = gstart[grp + 1] - o0;      // the group's slots in `order`
     __syncthreads();                                           // the previous group's activations are done with
     if (tid < 8) xmax[tid] = 0;
     __syncthreads();
-    const int c8 = p.K >> 3;
-    for (int r = 0; r < n; ++r) {
-      const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+    const int c8 = p.K >> 3;                                   // eight-column pieces of a row: a multiple of 16
+    auto piece_max = [&](const float (&f)[8]) {                // largest finite magnitude; infinities and NaN stay what they are below
       uint32_t m = 0;
-      for (int c = tid; c < c8; c += kMvThreads) {
-        float f[8];
-        mv_load8<kDt>(p.x, base + 8 * c, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
-          if (b < 0x7F800000u) m = max(m, b);                  // infinities and NaN stay what they are below
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+        if (b < 0x7F800000u) m = max(m, b);
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0 && m) atomicMax(&xmax[r], m);
-    }
-    __syncthreads();
+      return m;
+    };
     // power of two that takes the largest magnitude to [2^12, 2^13): exponent field of its inverse
     auto inv_exp = [&](int r) {
       const int ef = int(xmax[r] >> 23);
       return ef == 0 ? 127 : min(254, max(1, 127 + 12 - (ef - 127)));
     };
-    for (int r = 0; r < n; ++r) {
-      const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+    auto put = [&](int r, int c, const float (&f)[8]) {
       const float inv = __uint_as_float(uint32_t(inv_exp(r)) << 23);
-      for (int c = tid; c < c8; c += kMvThreads) {
-        float f[8];
-        mv_load8<kDt>(p.x, base + 8 * c, f);
-        uint32_t h[4];
+      uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
-        *reinterpret_cast<uint4*>(xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
+      *reinterpret_cast<uint4*>(xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+    };
+    if (n * c8 <= 2 * kMvThreads) {
+      // a piece or two a thread: held in registers between the two steps
+      float f[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = tid + i * kMvThreads, r = at / c8, c = at - r * c8;
+        if (at < n * c8) mv_load8<kDt>(p.x, int64_t(order[o0 + r] / p.x_div) * p.K + 8 * c, f[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = tid + i * kMvThreads;
+        uint32_t m = at < n * c8 ? piece_max(f[i]) : 0;        // (sixteen lanes share a row)
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((lane & 15) == 0 && m) atomicMax(&xmax[at / c8], m);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = tid + i * kMvThreads, r = at / c8;
+        if (at < n * c8) put(r, at - r * c8, f[i]);
+      }
+    } else {
+      for (int r = 0; r < n; ++r) {
+        const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+        uint32_t m = 0;
+        for (int c = tid; c < c8; c += kMvThreads) {
+          float f[8];
+          mv_load8<kDt>(p.x, base + 8 * c, f);
+          m = max(m, piece_max(f));
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0 && m) atomicMax(&xmax[r], m);
+      }
+      __syncthreads();
+      for (int r = 0; r < n; ++r) {
+        const int64_t base = int64_t(order[o0 + r] / p.x_div) * p.K;
+        for (int c = tid; c < c8; c += kMvThreads) {
+          float f[8];
+          mv_load8<kDt>(p.x, base + 8 * c, f);
+          put(r, c, f);
+        }
       }
     }
     float xscale[2];                                           // 2^exponent of columns 2q, 2q + 1
@@ -564,17 +631,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
 // whose expert id is out of range adds nothing.
 template <int kDt>
 __global__ void __launch_bounds__(128)
-fp4_combine_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids, const float* __restrict__ w, int k,
+fp4_combine_kernel(const float* y, const int32_t* __restrict__ ids, const float* __restrict__ w, int k,
                    int E, int D, uint16_t* __restrict__ out) {
   const int64_t t = blockIdx.y;
   const int c = (blockIdx.x * 128 + threadIdx.x) * 4;
+  wait_dependency();
   if (c >= D) return;
   float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int j = 0; j < k; ++j) {
     const int e = ids[t * k + j];
-    if (e < 0 || e >= E) continue;
     const float wj = w[t * k + j];
-    const float4 v = *reinterpret_cast<const float4*>(y + (t * k + j) * D + c);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const bool ok = e >= 0 && e < E;
+    if (ok) v = *reinterpret_cast<const float4*>(y + (t * k + j) * D + c);
+    if (!ok) continue;
     a[0] = fmaf(wj, v.x, a[0]);
     a[1] = fmaf(wj, v.y, a[1]);
     a[2] = fmaf(wj, v.z, a[2]);

@@ -93,8 +93,25 @@ int mv_group(int64_t K, int E, int S) {
   return 0;
 }
 
+// A launch that may start while the one before it in the stream drains
+// (`after`: that one is this call's own and announced it).
+template <typename K, typename... A>
+cudaError_t launch_after(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool after, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int kDt, bool kGated, int kOut>
-int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream) {
+int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream, bool after = false) {
   static std::atomic<uint64_t> done{0};
   auto kern = fp4_matvec_kernel<kDt, kGated, kOut>;
   MX_TRY(ensure_smem(kern, done, 232448 - 1024));
@@ -104,8 +121,7 @@ int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream) {
   a.team_warps = kMvWarps & -kMvWarps;
   while (a.team_warps > 1 && a.team_warps * 4 > a.K / 128) a.team_warps >>= 1;
   const int grid = int(std::min<int64_t>(int64_t(a.S) * a.tiles, d->sms));
-  kern<<<grid, kMvThreads, mv_smem(a.K, a.group, a.E, a.S), stream>>>(a);
-  MX_CHECK_CUDA(cudaGetLastError(), "4-bit matvec launch");
+  MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S), stream, after, a), "4-bit matvec launch");
   return MXMOE_OK;
 }
 
@@ -365,12 +381,12 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.codes = qw->w2_codes;
   a.scales = qw->w2_scales;
   a.out = ws.y;
-  MX_TRY((launch_mv<2, false, 2>(a, d, stream)));
+  MX_TRY((launch_mv<2, false, 2>(a, d, stream, true)));
   const dim3 grid(unsigned((D / 4 + 127) / 128), unsigned(T));
   auto* o = static_cast<uint16_t*>(out_tokens);
-  if (dtype == MXMOE_BF16) fp4_combine_kernel<kBF16><<<grid, 128, 0, stream>>>(ws.y, topk_ids, topk_weights, top_k, E, int(D), o);
-  else fp4_combine_kernel<kFP16><<<grid, 128, 0, stream>>>(ws.y, topk_ids, topk_weights, top_k, E, int(D), o);
-  MX_CHECK_CUDA(cudaGetLastError(), "decode combine launch");
+  const auto combine = dtype == MXMOE_BF16 ? fp4_combine_kernel<kBF16> : fp4_combine_kernel<kFP16>;
+  MX_CHECK_CUDA(launch_after(combine, grid, 128, 0, stream, true, static_cast<const float*>(ws.y), topk_ids, topk_weights,
+                             top_k, E, int(D), o), "decode combine launch");
   return MXMOE_OK;
 }
 
