@@ -68,12 +68,13 @@ struct Cfg {
   static constexpr int EPI_WARP_BYTES = 2048;  // one 32 x 32 block of 16-bit outputs per warp
   static constexpr int OFF_BAR = OFF_EPI + 8 * EPI_WARP_BYTES;
   static constexpr int NUM_BARS = 3 * kStages + 4;
-  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) & ~15;
   // offsets [E + 1]; first token tile of each expert [E + 1] (kWgrad: its rows); kWgrad's schedule order [E]
   static constexpr int TAB = (kMaxE + 4) * 4;
   static constexpr int OFF_TAB = OFF_MISC + 16;
   static constexpr int SMEM_BYTES = OFF_TAB + 2 * TAB + kMaxE * 2 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(OFF_TAB % 16 == 0 && TAB % 16 == 0, "the tables are read 16 bytes at a time");
 };
 
 // Instruction descriptor, kind::f16: fp32 accumulator (bit 4), A and B type at
