@@ -179,8 +179,10 @@ fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restr
 // The activations become f16 after a division by a power of two per slot that
 // puts the row's largest magnitude at 2^12: bf16 and fp16 inputs keep every
 // bit down to 2^-36 of the row's largest value (an absolute error of at most
-// 2^-37 of it beyond); the fp32 h between the two products is rounded to f16's
-// 11 bits, an eighth of the bf16 rounding of the result.
+// 2^-37 of it beyond).  The fp32 h between the two products of a layer becomes
+// one f16 (11 bits) where the result is bf16, of whose rounding that is an
+// eighth; where it is fp16, whose error it would raise by 1.4, h goes in as
+// two f16 pieces (22 bits) and takes twice the MMAs.
 //
 // Bound by HBM: (1/2 + 1/32) N K bytes per expert that has a slot.  A block of
 // 12 warps per SM walks a contiguous range of (slot group, row tile) units;
@@ -216,9 +218,12 @@ struct MvArgs {
   void* out;                // gated: fp32 h [S, 8 * tiles]; else y [S, 16 * tiles]
 };
 
-__host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S) {
+// Types of the activations: kBF16, kFP16, fp32 as one f16 piece, fp32 as two.
+constexpr int kF32 = 2, kF32Two = 3;
+
+__host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S, int pieces) {
   // ring, partial sums (two tiles), f16 activations, then counts, slot order, groups
-  return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 + 64 + (E + 1) * 4 + (4 * S + 1) * 4 + 256);
+  return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 * pieces + 64 + (E + 1) * 4 + (4 * S + 1) * 4 + 256);
 }
 
 // Programmatic dependent launch: the next launch of the stream may start its
@@ -235,9 +240,9 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-template <int kDt>   // kBF16, kFP16, or 2 for fp32
+template <int kDt>
 __device__ __forceinline__ void mv_load8(const void* x, int64_t i, float (&f)[8]) {
-  if constexpr (kDt == 2) {
+  if constexpr (kDt >= kF32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
     const float4 a = p[0], b = p[1];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -268,14 +273,16 @@ __device__ __forceinline__ void mma_f16_16816_zero(float (&c)[4], uint32_t a0, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-template <int kDt, bool kGated, int kOut>   // kOut: type of a non-gated result (kBF16, kFP16, 2 = fp32)
+template <int kDt, bool kGated, int kOut>   // kOut: type of a non-gated result (kBF16, kFP16, kF32)
 __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs p) {
   extern __shared__ __align__(128) uint8_t mv_smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   uint8_t* ring = mv_smem_raw;                                                    // [warp][slot]: codes, then scales
   float4* red = reinterpret_cast<float4*>(ring + kMvWarps * kMvRing * kMvSlot);   // [2][warp][lane]
   uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * kMvWarps * 32);              // f16 [K/32][group][4 quarters][8]
-  uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + int64_t(p.group) * p.K * 2);  // [8] largest magnitude, fp32 bits
+  constexpr int kPieces = kDt == kF32Two ? 2 : 1;
+  const int plane = p.group * p.K * 2;                                            // bytes of one f16 piece of the group
+  uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + kPieces * plane);              // [8] largest magnitude, fp32 bits
   int* order = reinterpret_cast<int*>(xmax + 16);                                 // [S] slots, group after group
   int* gexp = order + p.S;                                                        // [S] expert of each group
   int* gstart = gexp + p.S;                                                       // [S + 1] its first place in `order`
@@ -483,10 +490,22 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     };
     auto put = [&](int r, int c, const float (&f)[8]) {
       const float inv = __uint_as_float(uint32_t(inv_exp(r)) << 23);
+      uint8_t* at = xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16;
       uint32_t h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
-      *reinterpret_cast<uint4*>(xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+      if constexpr (kPieces == 2) {
+        // what the first piece left (of an infinity: nothing)
+        uint32_t l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = unpack16x2<kFP16>(h[j]);
+          const float a = f[2 * j] * inv, b = f[2 * j + 1] * inv;
+          l[j] = pack16x2<kFP16>(isinf(a) ? 0.0f : a - v.x, isinf(b) ? 0.0f : b - v.y);
+        }
+        *reinterpret_cast<uint4*>(at + plane) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
     };
     if (n * c8 <= 2 * kMvThreads) {
       // a piece or two a thread: held in registers between the two steps
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     __syncthreads();
     // this lane's column of a 32-block; columns past the group's slots read one zero piece
     const uint32_t xlane = g < n ? sm100::smem_u32(xs) + (g * 4 + q) * 16 : sm100::smem_u32(&zero);
-    const int xstep = g < n ? p.group * 64 : 0;
+    const int xstep = g < n ? p.group * 64 : 0, xplane = g < n ? plane : 0;
     int buf = 0;
     for (int64_t tile = tile0 + team; tile < tile1; tile += teams) {
       // ---- this warp's cells of the tile
@@ -582,6 +601,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
             float d[4];
             mma_f16_16816_zero(d, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
             mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
+            if constexpr (kPieces == 2) {
+              const uint4 xl = lds128(xb + (4 * c + j) * xstep + xplane);
+              mma_f16_16816(d, ha[0], hb[0], ha[1], hb[1], xl.x, xl.y);
+              mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xl.z, xl.w);
+            }
             acc[0] = fmaf(d[0], fa[j], acc[0]);
             acc[1] = fmaf(d[1], fa[j], acc[1]);
             acc[2] = fmaf(d[2], fb[j], acc[2]);
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         const float lo = (i ? t.y : t.x) * xscale[i], hi = (i ? t.w : t.z) * xscale[i];
         if constexpr (kGated) {
           static_cast<float*>(p.out)[s * p.tiles * 8 + tile * 8 + g] = silu_mul(lo, hi);
-        } else if constexpr (kOut == 2) {
+        } else if constexpr (kOut == kF32) {
           float* y = static_cast<float*>(p.out) + s * p.tiles * 16 + tile * 16 + g;
           y[0] = lo;
           y[8] = hi;

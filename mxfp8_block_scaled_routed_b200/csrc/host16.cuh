@@ -87,9 +87,9 @@ int check_ragged(int64_t M, int64_t N, int64_t K, int E, const int32_t* offsets,
 // ---------------------------------------------------------------- 4-bit matvec
 // Slots that share one pass over an expert's weights: eight, or as many as
 // shared memory holds next to the rings (0: not even one).
-int mv_group(int64_t K, int E, int S) {
+int mv_group(int64_t K, int E, int S, int pieces) {
   for (int g = 8; g >= 1; g >>= 1)
-    if (mv_smem(K, g, E, S) <= 232448 - 1024) return g;
+    if (mv_smem(K, g, E, S, pieces) <= 232448 - 1024) return g;
   return 0;
 }
 
@@ -115,13 +115,14 @@ int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream, bool after = fals
   static std::atomic<uint64_t> done{0};
   auto kern = fp4_matvec_kernel<kDt, kGated, kOut>;
   MX_TRY(ensure_smem(kern, done, 232448 - 1024));
-  a.group = mv_group(a.K, a.E, a.S);
+  constexpr int kPieces = kDt == kF32Two ? 2 : 1;
+  a.group = mv_group(a.K, a.E, a.S, kPieces);
   if (a.group == 0) return fail(MXMOE_ERR_SHAPE, "K=%d with E=%d and %d slots does not fit shared memory", a.K, a.E, a.S);
   // as many warps share a tile as leave each four cells or more of it
   a.team_warps = kMvWarps & -kMvWarps;
   while (a.team_warps > 1 && a.team_warps * 4 > a.K / 128) a.team_warps >>= 1;
   const int grid = int(std::min<int64_t>(int64_t(a.S) * a.tiles, d->sms));
-  MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S), stream, after, a), "4-bit matvec launch");
+  MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S, kPieces), stream, after, a), "4-bit matvec launch");
   return MXMOE_OK;
 }
 
@@ -307,7 +308,7 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
   MX_TRY(check_mult("K", K, 128));
   MX_TRY(check_mult("N", N, 16));
   if (K >= (1 << 24) || N >= (1 << 28)) return fail(MXMOE_ERR_SHAPE, "K=%lld N=%lld: too large", (long long)K, (long long)N);
-  if (S > 0 && mv_group(K, E, int(S)) == 0) return fail(MXMOE_ERR_SHAPE, "K=%lld does not fit shared memory", (long long)K);
+  if (S > 0 && mv_group(K, E, int(S), 1) == 0) return fail(MXMOE_ERR_SHAPE, "K=%lld does not fit shared memory", (long long)K);
   if (S == 0) return MXMOE_OK;
   MX_TRY(check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales}, {"y", y}}));
   if (!expert_ids) return fail(MXMOE_ERR_NULL, "expert_ids is NULL");
@@ -347,7 +348,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   MX_TRY(check_mult("F", F, 128));
   if (D >= (1 << 24) || F >= (1 << 24)) return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld: too large", (long long)D, (long long)F);
   if (T == 0) return MXMOE_OK;
-  if (mv_group(std::max(D, F), E, int(S)) == 0)
+  if (mv_group(D, E, int(S), 1) == 0 || mv_group(F, E, int(S), dtype == MXMOE_FP16 ? 2 : 1) == 0)
     return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld with %lld slots does not fit shared memory", (long long)D, (long long)F, (long long)S);
   if (!qw) return fail(MXMOE_ERR_NULL, "qweights is NULL");
   MX_TRY(check_ptrs({{"x_tokens", x_tokens}, {"out_tokens", out_tokens}, {"qw.w13_codes", qw->w13_codes},
@@ -372,7 +373,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.codes = qw->w13_codes;
   a.scales = qw->w13_scales;
   a.out = ws.h;
-  MX_TRY((dtype == MXMOE_BF16 ? launch_mv<kBF16, true, 2>(a, d, stream) : launch_mv<kFP16, true, 2>(a, d, stream)));
+  MX_TRY((dtype == MXMOE_BF16 ? launch_mv<kBF16, true, kF32>(a, d, stream) : launch_mv<kFP16, true, kF32>(a, d, stream)));
   // FC2: y [S, D] in fp32
   a.x = ws.h;
   a.x_div = 1;
@@ -381,7 +382,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.codes = qw->w2_codes;
   a.scales = qw->w2_scales;
   a.out = ws.y;
-  MX_TRY((launch_mv<2, false, 2>(a, d, stream, true)));
+  MX_TRY((dtype == MXMOE_BF16 ? launch_mv<kF32, false, kF32>(a, d, stream, true) : launch_mv<kF32Two, false, kF32>(a, d, stream, true)));
   const dim3 grid(unsigned((D / 4 + 127) / 128), unsigned(T));
   auto* o = static_cast<uint16_t*>(out_tokens);
   const auto combine = dtype == MXMOE_BF16 ? fp4_combine_kernel<kBF16> : fp4_combine_kernel<kFP16>;

@@ -199,7 +199,8 @@ def _layer(r, T, k, E, D, F, dt, distinct=True):
 
 
 def _layer_ref(w13, w2, ids, x, wt, dt):
-    """(result, bound): f16's half step on h, fp32's sums in both products and the combine, one rounding."""
+    """(result, bound): f16's half step on h (fp16 layers: of its second piece), fp32's sums in both products and the combine,
+    one rounding."""
     T, k = ids.shape
     F = w2.shape[2]
     out, err = torch.zeros(T, x.shape[1], dtype=torch.float64), torch.zeros(T, x.shape[1], dtype=torch.float64)
@@ -213,7 +214,7 @@ def _layer_ref(w13, w2, ids, x, wt, dt):
             h = a * s * b
             # |d silu / da| <= 1.1; the sigmoid's own error; products
             eh = 1.1 * ea * (b.abs() + eb) + (a * s).abs() * eb + (P.sigmoid_err(a) + 2.0 ** -22) * h.abs()
-            eh = eh + 2.0 ** -11 * (h.abs() + eh) + h.abs().max() * 2.0 ** -37
+            eh = eh + 2.0 ** (-11 if dt == BF else -22) * (h.abs() + eh) + h.abs().max() * 2.0 ** -37
             y = w2[e] @ h
             m = w2[e].abs() @ (h.abs() + eh)
             out[t] += wt[t, j].double() * y
