@@ -15,7 +15,11 @@
  * around it the token dispatcher (routing to the padded expert-major layout,
  * gather fused with the cast, weighted combine and its gradients; the
  * moe_layer_* composites run the whole token-major layer), the standalone
- * casts and dequantization (E4M3, and E5M2 for the transport payload).
+ * casts and dequantization (E4M3, and E5M2 for the transport payload).  Beside
+ * the MXFP8 path: the experts' products on 16-bit operands over unpadded
+ * segments with their gradients, a SwiGLU that keeps its input in 8 bits for
+ * the backward pass, and 4-bit (MXFP4) expert weights with the matrix-vector
+ * products and the layer of one to a few tokens.
  *
  * MXFP8 format (A2E MXFP8 pages, "quant_mode=4 ... E4M3 ... E8M0 MX scale"):
  * each block of 32 consecutive elements is stored as 32 E4M3 codes (uint8)
@@ -79,8 +83,8 @@ typedef enum {
 const char* mxmoe_last_error_message(void);
 
 /* Device-side error word of the current device.  Kernels set it when they
- * find a bad table (GEMMs: an offsets table -> MXMOE_ERR_OFFSETS; route: an
- * expert id outside [0, E) -> MXMOE_ERR_ARG, a layout past m_cap ->
+ * find a bad table (GEMMs: an offsets table -> MXMOE_ERR_OFFSETS; route and the
+ * 4-bit products: an expert id outside [0, E) -> MXMOE_ERR_ARG, a layout past m_cap ->
  * MXMOE_ERR_SHAPE; gather/combine: a slot or row out of range ->
  * MXMOE_ERR_OFFSETS) or when a bounded mbarrier wait expires
  * (MXMOE_ERR_DEVICE_TIMEOUT).
@@ -509,8 +513,9 @@ int moe_layer_bwd_q(const void* dout_tokens, int64_t T, int64_t D, const float* 
  *                  mxmoe_check_device_error().
  *  Rows at or past offsets[E] are not written, and what they hold (NaN, say)
  *  has no effect.  out must not overlap a or w.
- *  Needs N and K multiples of 8, E <= 1024, 0 <= M < 2^31 (M == 0: nothing is
- *  done), 16-byte aligned tensors.
+ *  Needs N and K multiples of 8, E <= 1024, 0 <= M <= 2^31 - 1024 (M == 0:
+ *  nothing is done), 16-byte aligned tensors.  Rows whose pitch is not a
+ *  multiple of 32 bytes (N or K odd multiples of 8) are loaded more slowly.
  * ------------------------------------------------------------------------- */
 int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N, int64_t K,
                       const int32_t* expert_offsets, int transpose_w, int dtype, void* out, cudaStream_t stream);
@@ -594,7 +599,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *  written).  Each expert's weights are read once per eight slots it has (fewer
  *  for K above 7168, as shared memory allows).  Products with f16 copies of x (a power of two per row keeps 16-bit inputs
  *  exact down to 2^-36 of the row's largest value), fp32 sums, one rounding.
- *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048.
+ *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048, S * N / 16 < 2^31, and
+ *  shared memory for one f16 row (K up to about 60000).
  * ------------------------------------------------------------------------- */
 int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expert_ids, const uint8_t* codes,
                         const uint8_t* scales, int E, int64_t N, int dtype, void* y, cudaStream_t stream);

@@ -630,17 +630,20 @@ def _dtype(t, name: str) -> int:
 
 
 def _like(t, ref, shape, dtype, name: str):
-    """t checked against a shape, a type and ref's device; None allocates it there."""
-    if t is None:
-        return ref.new_empty(shape, dtype=dtype)
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == ref.device and t.is_contiguous():
+    """t checked against a shape (None: any), a type and ref's device."""
+    if type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape) and t.device == ref.device and t.is_contiguous():
         return t                                       # (ref is a CUDA tensor; below: which of these it was)
     _need(t, dtype, name)
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != ref.device:
         raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
     return t
+
+
+def _out(t, ref, shape, dtype, name: str):
+    """An output: the caller's, checked, or a new one on ref's device."""
+    return ref.new_empty(shape, dtype=dtype) if t is None else _like(t, ref, shape, dtype, name)
 
 
 def _call(fn, ref, *args):
@@ -664,13 +667,13 @@ def mxmoe_ragged_gemm(a, w, offsets, transpose_w=False, out=None):
     dt = _dtype(a, "a")
     if a.dim() != 2:
         raise ValueError("a must be 2-D")
-    _like(offsets, a, offsets.shape, torch.int32, "offsets")
+    _like(offsets, a, None, torch.int32, "offsets")
+    _like(w, a, None, a.dtype, "w")
     E = offsets.numel() - 1
     if w.dim() != 3 or w.shape[0] != E or w.shape[1 if transpose_w else 2] != a.shape[1]:
         raise ValueError(f"w must be [E={E}, N, K] with {'N' if transpose_w else 'K'}={a.shape[1]}, got {tuple(w.shape)}")
-    _like(w, a, w.shape, a.dtype, "w")
     M, (_, N, K) = a.shape[0], w.shape
-    out = _like(out, a, (M, K if transpose_w else N), a.dtype, "out")
+    out = _out(out, a, (M, K if transpose_w else N), a.dtype, "out")
     _call(lib().mxmoe_ragged_gemm, a, a.data_ptr(), M, w.data_ptr(), E, N, K, offsets.data_ptr(), int(bool(transpose_w)),
           dt, out.data_ptr())
     return out
@@ -681,14 +684,14 @@ def mxmoe_ragged_gemm_wgrad(g, a, offsets, out=None):
 
     An expert without rows gets exact zeros."""
     dt = _dtype(g, "g")
-    if g.dim() != 2 or a.dim() != 2:
-        raise ValueError("g and a must be 2-D")
+    _like(a, g, None, g.dtype, "a")
+    _like(offsets, g, None, torch.int32, "offsets")
+    if g.dim() != 2 or a.dim() != 2 or a.shape[0] != g.shape[0]:
+        raise ValueError(f"g must be [M, N] and a [M, K], got {tuple(g.shape)} and {tuple(a.shape)}")
     M, N = g.shape
     K = a.shape[1]
-    _like(a, g, (M, K), g.dtype, "a")
-    _like(offsets, g, offsets.shape, torch.int32, "offsets")
     E = offsets.numel() - 1
-    out = _like(out, g, (E, N, K), g.dtype, "out")
+    out = _out(out, g, (E, N, K), g.dtype, "out")
     _call(lib().mxmoe_ragged_gemm_wgrad, g, g.data_ptr(), N, a.data_ptr(), K, M, offsets.data_ptr(), E, dt,
           out.data_ptr())
     return out
@@ -706,9 +709,9 @@ def mxfp8_swiglu_ckpt(h13, rows_dev=None, h=None, codes=None, scales=None):
     rows, F = h13.shape[0], h13.shape[1] // 2
     if rows_dev is not None:
         _like(rows_dev, h13, (1,), torch.int32, "rows_dev")
-    h = _like(h, h13, (rows, F), h13.dtype, "h")
-    codes = _like(codes, h13, (rows, 2 * F), torch.uint8, "codes")
-    scales = _like(scales, h13, (rows, 2, (F + 31) // 32), torch.uint8, "scales")
+    h = _out(h, h13, (rows, F), h13.dtype, "h")
+    codes = _out(codes, h13, (rows, 2 * F), torch.uint8, "codes")
+    scales = _out(scales, h13, (rows, 2, (F + 31) // 32), torch.uint8, "scales")
     _call(lib().mxfp8_swiglu_ckpt, h13, h13.data_ptr(), rows, F, None if rows_dev is None else rows_dev.data_ptr(), dt,
           h.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return dict(h=h, codes=codes, scales=scales)
@@ -726,9 +729,9 @@ def mxfp8_swiglu_ckpt_bwd(dh, codes, scales, rows_dev=None, dh13=None, h=None, w
     _like(scales, dh, (rows, 2, (F + 31) // 32), torch.uint8, "scales")
     if rows_dev is not None:
         _like(rows_dev, dh, (1,), torch.int32, "rows_dev")
-    dh13 = _like(dh13, dh, (rows, 2 * F), dh.dtype, "dh13")
+    dh13 = _out(dh13, dh, (rows, 2 * F), dh.dtype, "dh13")
     if want_h or h is not None:
-        h = _like(h, dh, (rows, F), dh.dtype, "h")
+        h = _out(h, dh, (rows, F), dh.dtype, "h")
     _call(lib().mxfp8_swiglu_ckpt_bwd, dh, dh.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, F,
           None if rows_dev is None else rows_dev.data_ptr(), dt, dh13.data_ptr(), None if h is None else h.data_ptr())
     return dict(dh13=dh13, h=h)
@@ -771,6 +774,7 @@ def mxfp4_expert_matvec(x, expert_ids, codes, scales, out=None):
     x [S, K] bf16 or fp16, expert_ids int32 [S], codes [E, N, K/2] and scales [E, N, K/32] in the TILE layout; y [S, N].
     For a few slots (at most 2048): each expert's weights are read once per eight of its slots."""
     dt = _dtype(x, "x")
+    _like(codes, x, None, torch.uint8, "codes")
     if x.dim() != 2 or codes.dim() != 3:
         raise ValueError("x must be [S, K] and codes [E, N, K/2]")
     S, K = x.shape
@@ -778,7 +782,7 @@ def mxfp4_expert_matvec(x, expert_ids, codes, scales, out=None):
     _like(expert_ids, x, (S,), torch.int32, "expert_ids")
     _like(codes, x, (E, N, K // 2), torch.uint8, "codes")
     _like(scales, x, (E, N, K // 32), torch.uint8, "scales")
-    out = _like(out, x, (S, N), x.dtype, "out")
+    out = _out(out, x, (S, N), x.dtype, "out")
     _call(lib().mxfp4_expert_matvec, x, x.data_ptr(), S, K, expert_ids.data_ptr(), codes.data_ptr(), scales.data_ptr(),
           E, N, dt, out.data_ptr())
     return out
@@ -786,6 +790,8 @@ def mxfp4_expert_matvec(x, expert_ids, codes, scales, out=None):
 
 def mxfp4_quantize_experts(w13, w2):
     """4-bit copies of W13 [E, 2F, D] and W2 [E, D, F] in the layouts that moe_layer_decode_fp4 reads."""
+    _dtype(w13, "w13")
+    _like(w2, w13, None, w13.dtype, "w2")
     if w13.dim() != 3 or w2.dim() != 3 or w13.shape != (w2.shape[0], 2 * w2.shape[2], w2.shape[1]):
         raise ValueError(f"w13 must be [E, 2F, D] and w2 [E, D, F], got {tuple(w13.shape)} and {tuple(w2.shape)}")
     a, b = mxfp4_quantize(w13, TILE_GATED), mxfp4_quantize(w2, TILE)
@@ -804,23 +810,26 @@ def moe_layer_decode_fp4(x_tokens, topk_ids, topk_weights, qw, out=None, workspa
     out[t] = sum_j topk_weights[t, j] * W2[e] . (silu(gate) * up), [gate | up] = W13[e] . x[t], e = topk_ids[t, j].
     workspace (optional): uint8, at least decode_workspace_bytes(T, top_k, D, F) long; calls that may overlap need one each."""
     dt = _dtype(x_tokens, "x_tokens")
-    if x_tokens.dim() != 2 or topk_ids.dim() != 2:
-        raise ValueError("x_tokens must be [T, D] and topk_ids [T, top_k]")
+    c13, c2 = qw["w13_codes"], qw["w2_codes"]
+    _like(topk_ids, x_tokens, None, torch.int32, "topk_ids")
+    _like(c13, x_tokens, None, torch.uint8, "qw['w13_codes']")
+    if x_tokens.dim() != 2 or topk_ids.dim() != 2 or c13.dim() != 3:
+        raise ValueError("x_tokens must be [T, D], topk_ids [T, top_k] and qw['w13_codes'] [E, 2F, D/2]")
     T, D = x_tokens.shape
     k = topk_ids.shape[1]
-    c13, c2 = qw["w13_codes"], qw["w2_codes"]
     E, F = c13.shape[0], c13.shape[1] // 2
-    _like(topk_ids, x_tokens, (T, k), torch.int32, "topk_ids")
+    if topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must have shape ({T}, top_k), got {tuple(topk_ids.shape)}")
     _like(topk_weights, x_tokens, (T, k), torch.float32, "topk_weights")
     _like(c13, x_tokens, (E, 2 * F, D // 2), torch.uint8, "qw['w13_codes']")
     _like(c2, x_tokens, (E, D, F // 2), torch.uint8, "qw['w2_codes']")
     _like(qw["w13_scales"], x_tokens, (E, 2 * F, D // 32), torch.uint8, "qw['w13_scales']")
     _like(qw["w2_scales"], x_tokens, (E, D, F // 32), torch.uint8, "qw['w2_scales']")
-    out = _like(out, x_tokens, (T, D), x_tokens.dtype, "out")
+    out = _out(out, x_tokens, (T, D), x_tokens.dtype, "out")
     if workspace is None:
         workspace = x_tokens.new_empty((decode_workspace_bytes(T, k, D, F),), dtype=torch.uint8)
     else:
-        _like(workspace, x_tokens, workspace.shape, torch.uint8, "workspace")
+        _like(workspace, x_tokens, None, torch.uint8, "workspace")
     st = _Q4Weights(c13.data_ptr(), qw["w13_scales"].data_ptr(), c2.data_ptr(), qw["w2_scales"].data_ptr())
     _call(lib().moe_layer_decode_fp4, x_tokens, x_tokens.data_ptr(), T, D, topk_ids.data_ptr(), topk_weights.data_ptr(), k,
           ctypes.byref(st), E, F, dt, out.data_ptr(), workspace.data_ptr(), workspace.numel())

@@ -209,9 +209,10 @@ struct MvArgs {
   int S;
   int x_div;                // slot s reads row s / x_div of x
   int E;
-  int64_t tiles;            // row tiles per expert
+  int tiles;                // row tiles per expert (S * tiles < 2^31)
   int K;
-  int team_warps;           // warps that share a tile's cells: 1, 2, 4, 8 or 16
+  int team_log2;            // warps that share a tile's cells: 1, 2 or 4 as a power of two (no divisions in a
+                            // block's first instructions, which come from L2)
   int group;                // slots per group, 1..8 (shared memory holds group * K f16)
   const uint8_t* codes;
   const uint8_t* scales;
@@ -389,26 +390,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   }
 
   // ---- units (group, tile), a contiguous range of them per block, cut into
-  // one segment per group; a segment's units go round the teams of `team_warps`
-  // warps, a unit's cells round the warps of a team
-  const int64_t units = int64_t(ngroups) * p.tiles;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  // one segment per group; a segment's units go round the teams of warps, a
+  // unit's cells are shared out to the warps of a team
+  const int units = ngroups * p.tiles, share = units / int(gridDim.x), over = units - share * int(gridDim.x);
+  const int u0 = share * int(blockIdx.x) + min(int(blockIdx.x), over), total = share + (int(blockIdx.x) < over);
   const int cells = p.K >> 7;                                  // 128-column cells of a tile
-  const int W = p.team_warps, teams = kMvWarps / W;
-  const int team = warp / W, member = warp % W;
+  const int W = 1 << p.team_log2, teams = kMvWarps >> p.team_log2, team = warp >> p.team_log2, member = warp & (W - 1);
   // this warp's cells of a tile, [cell0, cell0 + mine)
-  const int cell0 = member * cells / W, mine = (member + 1) * cells / W - cell0;
+  const int cell0 = (member * cells) >> p.team_log2, mine = (((member + 1) * cells) >> p.team_log2) - cell0;
   const uint32_t ring_at = sm100::smem_u32(ring) + warp * kMvRing * kMvSlot;
-  const int grp0 = u1 > u0 ? int(u0 / p.tiles) : 0;
-  const int64_t first_tile = u0 - grp0 * p.tiles, total = u1 - u0;
+  const int grp0 = u0 / p.tiles, first_tile = u0 - grp0 * p.tiles;
   // (segment i of this block: group grp0 + i, tiles [tile0, tile1))
 
   // ---- the warp's next cell to load: `left` units from the start of its
   // segment on, (ld_grp, ld_tile, ld_i) its place
-  int64_t left = mine > 0 ? total : 0, ld_tile0 = first_tile, ld_tile = 0, ld_tile1 = 0;
-  int ld_grp = grp0, ld_i = 0, ld_slot = 0;
+  int left = mine > 0 ? total : 0, ld_tile0 = first_tile, ld_tile = 0, ld_tile1 = 0, ld_grp = grp0, ld_i = 0, ld_slot = 0;
   const uint8_t *ld_codes = nullptr, *ld_scales = nullptr;
-  const int64_t jump = int64_t(teams) * cells - mine;          // from behind a unit's last cell to the next unit's first
+  const int jump = teams * cells - mine;          // from behind a unit's last cell to the next unit's first
   auto to_segment = [&]() {                                    // to the team's first unit at or after the segment's start
     ld_tile = ld_tile0 + team;
     ld_tile1 = min(p.tiles, ld_tile0 + left);
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       ld_tile1 = min(p.tiles, left);
     }
     if (left > 0) {
-      const int64_t cell = (gexp[ld_grp] * p.tiles + ld_tile) * cells + cell0;
+      const int64_t cell = (int64_t(gexp[ld_grp]) * p.tiles + ld_tile) * cells + cell0;
       ld_codes = p.codes + cell * 1024 + lane * 16;
       ld_scales = p.scales + cell * 64 + (lane & 7) * 16;
     }
@@ -437,14 +435,14 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       }
       if (lane < 4 * nc) cp_async16(dst + kMvCells * 1024, ld_scales);
       ld_i += nc;
-      int64_t step = nc;
+      int step = nc;
       if (ld_i == mine) {
         ld_i = 0;
         step += jump;
         ld_tile += teams;
       }
-      ld_codes += step * 1024;
-      ld_scales += step * 64;
+      ld_codes += int64_t(step) * 1024;
+      ld_scales += int64_t(step) * 64;
       if (ld_tile >= ld_tile1) {                               // on to the next group's segment
         left -= ld_tile1 - ld_tile0;
         ld_tile0 = 0;
@@ -456,17 +454,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     if (++ld_slot == kMvRing) ld_slot = 0;
   };
   if (left > 0) to_segment();
+#pragma unroll 1   // (one copy: a block's first instructions come from L2)
   for (int i = 0; i < kMvRing; ++i) load_next();
   // up to here only the ids and the weights were read; x may be the result of
   // the launch before this one
   wait_dependency();
 
-  int64_t done = 0;                                            // units of the segments before the current one
+  int done = 0;                                                // units of the segments before the current one
   int slot = 0;
   float4* tred = red + team * 2 * W * 32;                      // this team's partial sums, two units deep
   for (int grp = grp0; done < total; ++grp) {
-    const int64_t tile0 = grp == grp0 ? first_tile : 0;
-    const int64_t tile1 = min(p.tiles, tile0 + (total - done));
+    const int tile0 = grp == grp0 ? first_tile : 0, tile1 = min(p.tiles, tile0 + (total - done));
     done += tile1 - tile0;
     // ---- this group's activations: row maxima, then f16 into shared memory
     const int o0 = gstart[grp], n = gstart[grp + 1] - o0;      // the group's slots in `order`
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     const uint32_t xlane = g < n ? sm100::smem_u32(xs) + (g * 4 + q) * 16 : sm100::smem_u32(&zero);
     const int xstep = g < n ? p.group * 64 : 0, xplane = g < n ? plane : 0;
     int buf = 0;
-    for (int64_t tile = tile0 + team; tile < tile1; tile += teams) {
+    for (int tile = tile0 + team; tile < tile1; tile += teams) {
       // ---- this warp's cells of the tile
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int i = 0; i < mine; i += kMvCells) {
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       if (W > 1) {
         tred[(buf * W + member) * 32 + lane] = t;
         sm100::named_bar_sync(1 + team, W * 32);
-        if (member != int(tile) % W) { buf ^= 1; continue; }
+        if (member != (tile & (W - 1))) { buf ^= 1; continue; }
         t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int w = 0; w < W; ++w) {
           const float4 v = tred[(buf * W + w) * 32 + lane];

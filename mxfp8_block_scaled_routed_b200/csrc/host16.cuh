@@ -75,7 +75,8 @@ int launch_ragged(int dtype, const CUtensorMap& ma, const CUtensorMap& mb, const
 
 int check_ragged(int64_t M, int64_t N, int64_t K, int E, const int32_t* offsets, int dtype) {
   MX_TRY(check_dtype(dtype));
-  if (M < 0 || M >= (int64_t(1) << 31)) return fail(MXMOE_ERR_SHAPE, "M=%lld must be in [0, 2^31)", (long long)M);
+  // (token numbers are 32-bit in the kernel, up to a tile past the last row)
+  if (M < 0 || M > (int64_t(1) << 31) - 1024) return fail(MXMOE_ERR_SHAPE, "M=%lld must be in [0, 2^31 - 1024]", (long long)M);
   if (E <= 0 || E > ragged::kMaxE) return fail(MXMOE_ERR_SHAPE, "E=%d must be in [1, %d]", E, ragged::kMaxE);
   MX_TRY(check_mult("N", N, 8));
   MX_TRY(check_mult("K", K, 8));
@@ -119,8 +120,8 @@ int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream, bool after = fals
   a.group = mv_group(a.K, a.E, a.S, kPieces);
   if (a.group == 0) return fail(MXMOE_ERR_SHAPE, "K=%d with E=%d and %d slots does not fit shared memory", a.K, a.E, a.S);
   // as many warps share a tile as leave each four cells or more of it
-  a.team_warps = kMvWarps & -kMvWarps;
-  while (a.team_warps > 1 && a.team_warps * 4 > a.K / 128) a.team_warps >>= 1;
+  a.team_log2 = kMvWarps % 4 == 0 ? 2 : 0;
+  while (a.team_log2 > 0 && (4 << a.team_log2) > a.K / 128) --a.team_log2;
   const int grid = int(std::min<int64_t>(int64_t(a.S) * a.tiles, d->sms));
   MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S, kPieces), stream, after, a), "4-bit matvec launch");
   return MXMOE_OK;
@@ -307,7 +308,7 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
   MX_TRY(check_mv(S, E));
   MX_TRY(check_mult("K", K, 128));
   MX_TRY(check_mult("N", N, 16));
-  if (K >= (1 << 24) || N >= (1 << 28)) return fail(MXMOE_ERR_SHAPE, "K=%lld N=%lld: too large", (long long)K, (long long)N);
+  if (K >= (1 << 24) || N >= (1 << 28) || S * (N / 16) > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "K=%lld N=%lld: too large", (long long)K, (long long)N);
   if (S > 0 && mv_group(K, E, int(S), 1) == 0) return fail(MXMOE_ERR_SHAPE, "K=%lld does not fit shared memory", (long long)K);
   if (S == 0) return MXMOE_OK;
   MX_TRY(check_ptrs({{"x", x}, {"codes", codes}, {"scales", scales}, {"y", y}}));
@@ -320,7 +321,7 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
   a.S = int(S);
   a.x_div = 1;
   a.E = E;
-  a.tiles = N / 16;
+  a.tiles = int(N / 16);
   a.K = int(K);
   a.codes = codes;
   a.scales = scales;
@@ -346,7 +347,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   MX_TRY(check_mv(S, E));
   MX_TRY(check_mult("D", D, 128));
   MX_TRY(check_mult("F", F, 128));
-  if (D >= (1 << 24) || F >= (1 << 24)) return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld: too large", (long long)D, (long long)F);
+  if (D >= (1 << 24) || F >= (1 << 24) || S * (std::max(D, F) / 8) > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld: too large", (long long)D, (long long)F);
   if (T == 0) return MXMOE_OK;
   if (mv_group(D, E, int(S), 1) == 0 || mv_group(F, E, int(S), dtype == MXMOE_FP16 ? 2 : 1) == 0)
     return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld with %lld slots does not fit shared memory", (long long)D, (long long)F, (long long)S);
@@ -368,7 +369,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   // FC1 + SwiGLU: h [S, F] in fp32
   a.x = x_tokens;
   a.x_div = top_k;
-  a.tiles = F / 8;
+  a.tiles = int(F / 8);
   a.K = int(D);
   a.codes = qw->w13_codes;
   a.scales = qw->w13_scales;
@@ -377,7 +378,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   // FC2: y [S, D] in fp32
   a.x = ws.h;
   a.x_div = 1;
-  a.tiles = D / 16;
+  a.tiles = int(D / 16);
   a.K = int(F);
   a.codes = qw->w2_codes;
   a.scales = qw->w2_scales;

@@ -29,7 +29,7 @@ def test_ragged_refusals(L):
         v = {**ok, **kw}
         return L.mxmoe_ragged_gemm(v["a"], v["M"], v["w"], v["E"], v["N"], v["K"], v["off"], v["tr"], v["dt"], v["out"], None)
 
-    for kw, status, word in ((dict(N=12), 2, "N=12"), (dict(K=0), 2, "K=0"), (dict(M=-1), 2, "M=-1"), (dict(M=1 << 31), 2, "M="),
+    for kw, status, word in ((dict(N=12), 2, "N=12"), (dict(K=0), 2, "K=0"), (dict(M=-1), 2, "M=-1"), (dict(M=(1 << 31) - 1023), 2, "M="),
                              (dict(E=0), 2, "E=0"), (dict(E=1025), 2, "E=1025"), (dict(off=None), 1, "expert_offsets"),
                              (dict(a=None), 1, "a is NULL"), (dict(w=MIS), 3, "w is not"), (dict(out=MIS), 3, "out is not"),
                              (dict(dt=2), 9, "dtype=2"), (dict(tr=3), 9, "transpose_w=3"), (dict(N=1 << 30), 2, "2^30")):
@@ -98,6 +98,8 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
             call()
     with pytest.raises(TypeError, match="bfloat16 or torch.float16"):
         mxk.mxfp4_quantize(x.float())
+    with pytest.raises(TypeError, match="a must be a torch.Tensor"):
+        mxk.mxmoe_ragged_gemm([1.0], x, x)
     with pytest.raises(TypeError, match="dtype"):
         mxk.mxfp4_dequantize(x, x, dtype=torch.float32)
 

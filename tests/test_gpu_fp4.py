@@ -309,3 +309,44 @@ def test_matvec_with_many_groups_of_an_expert(S, E, N, K):
     c, s = _tiled(packed, byte, False)
     y = mxk.mxfp4_expert_matvec(x.to(DEV, BF), torch.from_numpy(ids).to(DEV), c, s)
     P.assert_same(y, torch.stack([w[ids[i]] @ x[i] for i in range(S)]).to(BF), "y")
+
+
+# ------------------------------------------------------------------------------------------------ refusals of the bindings
+def test_bindings_refuse_wrong_tensors():
+    g = lambda *s, dt=BF: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    u8 = lambda *s: g(*s, dt=torch.uint8)  # noqa: E731
+    i32 = lambda *s: g(*s, dt=torch.int32)  # noqa: E731
+    qw = dict(w13_codes=u8(2, 256, 64), w13_scales=u8(2, 256, 4), w2_codes=u8(2, 128, 64), w2_scales=u8(2, 128, 4))
+    x, ids, wt = g(3, 128), i32(3, 2), torch.zeros(3, 2, device=DEV)
+    cases = [
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 24), off)),                       # K differs
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(3, 8, 16), off)),                       # E differs
+        (TypeError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 16, dt=FP), off)),                 # types differ
+        (TypeError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 16), off.long())),
+        (TypeError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 16), None)),
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm(g(4, 32)[:, ::2], g(2, 8, 16), off)),               # not contiguous
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 16), off, out=g(4, 16))),
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm(g(4, 16), g(2, 8, 16), off.cpu())),
+        (mxk.MXMOEError, lambda: mxk.mxmoe_ragged_gemm(g(4, 12), g(2, 8, 12), off)),
+        (mxk.MXMOEError, lambda: mxk.mxmoe_ragged_gemm(g(65)[1:].view(4, 16), g(2, 8, 16), off)),      # not 16-byte aligned
+        (ValueError, lambda: mxk.mxmoe_ragged_gemm_wgrad(g(4, 16), g(5, 8), off)),
+        (ValueError, lambda: mxk.mxfp8_swiglu_ckpt(g(4, 15))),
+        (mxk.MXMOEError, lambda: mxk.mxfp8_swiglu_ckpt(g(4, 24))),
+        (TypeError, lambda: mxk.mxfp8_swiglu_ckpt_bwd(g(4, 16), None, None)),
+        (ValueError, lambda: mxk.mxfp8_swiglu_ckpt_bwd(g(4, 16), u8(4, 32), u8(4, 2))),
+        (mxk.MXMOEError, lambda: mxk.mxfp4_quantize(g(4, 48))),
+        (mxk.MXMOEError, lambda: mxk.mxfp4_quantize(g(24, 128), mxk.TILE)),
+        (ValueError, lambda: mxk.mxfp4_dequantize(u8(4, 32), u8(4, 3))),
+        (ValueError, lambda: mxk.mxfp4_expert_matvec(x, i32(4), u8(2, 16, 64), u8(2, 16, 4))),
+        (ValueError, lambda: mxk.mxfp4_expert_matvec(x, i32(3), u8(2, 16, 32), u8(2, 16, 4))),
+        (ValueError, lambda: mxk.moe_layer_decode_fp4(x, i32(2, 2), wt, qw)),
+        (ValueError, lambda: mxk.moe_layer_decode_fp4(x, ids, wt[:, :1].contiguous(), qw)),
+        (mxk.MXMOEError, lambda: mxk.moe_layer_decode_fp4(x, ids, wt, qw, workspace=u8(16))),
+        (ValueError, lambda: mxk.mxfp4_quantize_experts(g(2, 256, 128), g(2, 128, 256))),
+    ]
+    for i, (err, call) in enumerate(cases):
+        with pytest.raises(err):
+            call()
+            pytest.fail(f"case {i} was accepted")
+    assert mxk.device_error() == 0
