@@ -185,21 +185,20 @@ fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restr
 // two f16 pieces (22 bits) and takes twice the MMAs.
 //
 // Bound by HBM: (1/2 + 1/32) N K bytes per expert that has a slot.  A block of
-// 12 warps per SM walks a contiguous range of (slot group, row tile) units;
+// 16 warps per SM walks a contiguous range of (slot group, row tile) units;
 // each warp takes its share of a tile's 128-column cells through its own ring
 // of cp.async loads (every lane reads back the codes it loaded itself), so the
 // loads of later tiles are in flight while this one is multiplied, and the
 // warps' partial sums meet in shared memory in a fixed order.
 // Measured on 46 of 64 experts of 7168 x 2048 (1.08 GB of weights, both
-// products and the combine): 214 us, 5.0 TB/s of weights; the loop without its
-// products 175 us.  What is left is issue (132 instructions a cell, of which
-// 32 conversions, 8 MMAs, 16 FMAs).  Bulk copies instead of cp.async: 236 us
-// (about 75 cycles of the issuing warp a copy; from one feeding warp 352 us);
-// one cell a load 228 us; 16 / 20 warps 217 / 215 us, and 2 to 3 us more on
-// one token.
-constexpr int kMvWarps = 12, kMvThreads = 32 * kMvWarps;
+// products and the combine): 198 us, 5.4 TB/s of weights; the loop without its
+// products 175 us.  What is left is issue (115 instructions a cell, of which 32
+// conversions, 8 MMAs, 16 FMAs).  12 warps with a ring of three 205 us; bulk
+// copies instead of cp.async 8 % more (about 75 cycles of the issuing warp a
+// copy; all of them from one feeding warp 60 % more); one cell a load 6 % more.
+constexpr int kMvWarps = 16, kMvThreads = 32 * kMvWarps;
 constexpr int kMvCells = 2;                 // neighbouring cells (16 x 128) that a warp loads together
-constexpr int kMvRing = 3;                  // such loads in flight per warp
+constexpr int kMvRing = 2;                  // such loads in flight per warp
 constexpr int kMvSlot = kMvCells * (1024 + 64);
 constexpr int kMvMaxSlots = 2048, kMvMaxE = 1024;
 
