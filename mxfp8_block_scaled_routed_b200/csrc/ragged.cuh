@@ -104,7 +104,8 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int
 }
 
 // One lane of a converged warp (the same one each time).  The TMA and MMA
-// roles run their loops with the whole warp and issue under this: inside an
+// roles run their loops with the whole warp (each wait's outcome is the
+// warp's) and issue under this: inside an
 // `if (lane == 0)` role a tcgen05.mma took its thread ~120 cycles to issue,
 // and a K block ~580 cycles however narrow its tile.
 __device__ __forceinline__ bool elect_one() {
@@ -292,7 +293,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const uint32_t bytes = C::A_BYTES + boxes * kCols * 128;       // per CTA
       const int r0 = T.r0 + rank * 128, b0 = rank * half;
       for (int kb = 0; kb < T.nk; ++kb) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1))) { ok = false; break; }
         if (elect_one()) {
           const uint32_t as = sbase + C::OFF_A + stage * C::A_BYTES, bs = sbase + C::OFF_B + stage * C::B_BYTES;
           uint32_t fb = mapa_cluster(full_bar(stage), 0);
@@ -350,12 +351,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
           if (more) next = get_tile<kMode>(p, offs, tab, ord, w.after());
           continue;
         }
-        if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1))) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::BN;
         const uint32_t idesc = f16_idesc(kDt == kBF16 ? 1 : 0, kAMn, kBMn, C::BM, uint32_t((T.n + 15) & ~15));
         for (int kb = 0; kb < T.nk; ++kb) {
-          if (!mbar_wait_cluster(full_bar(stage), phase)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(full_bar(stage), phase))) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
             const uint64_t ad = a_desc + stage * (C::A_BYTES >> 4), bd = b_desc + stage * (C::B_BYTES >> 4);
