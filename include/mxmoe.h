@@ -518,7 +518,16 @@ int moe_layer_bwd_q(const void* dout_tokens, int64_t T, int64_t D, const float* 
  *  multiple of 32 bytes (N or K odd multiples of 8) are loaded more slowly.
  * ------------------------------------------------------------------------- */
 int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N, int64_t K,
-                      const int32_t* expert_offsets, int transpose_w, int dtype, void* out, cudaStream_t stream);
+                      const int32_t* expert_offsets, int transpose_w, int dtype, void* out,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace with which a ragged product is split along its
+ * contraction and joined by a second launch (few tiles, a long contraction);
+ * 0: it is not split.  which: 0 and 1 mxmoe_ragged_gemm with that transpose_w,
+ * 2 mxmoe_ragged_gemm_wgrad.  workspace may be NULL: the product runs unsplit
+ * (the sums then round in another order).  Calls that may overlap on the GPU
+ * need a workspace each. */
+size_t mxmoe_ragged_workspace_size(int64_t M, int64_t N, int64_t K, int E, int which);
 
 /* -------------------------------------------------------------------------
  * mxmoe_ragged_gemm_wgrad -- weight gradient of mxmoe_ragged_gemm.
@@ -529,7 +538,8 @@ int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N,
  *  all of them).  Segments and limits as mxmoe_ragged_gemm.
  * ------------------------------------------------------------------------- */
 int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, int64_t M,
-                            const int32_t* expert_offsets, int E, int dtype, void* dw, cudaStream_t stream);
+                            const int32_t* expert_offsets, int E, int dtype, void* dw,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* -------------------------------------------------------------------------
  * mxfp8_swiglu_ckpt -- SwiGLU that keeps its input in 8 bits.

@@ -99,8 +99,9 @@ _SIGS = {
                          ctypes.POINTER(_LayerSaved), _P, _S, _P], _I),
     "moe_layer_bwd_q": ([_P, _L, _L, _P, _I, ctypes.POINTER(_QWeights), _I, _L, _I, ctypes.POINTER(_LayerSaved),
                          _P, _P, _P, _P, _P, _S, _P], _I),
-    "mxmoe_ragged_gemm": ([_P, _L, _P, _I, _L, _L, _P, _I, _I, _P, _P], _I),
-    "mxmoe_ragged_gemm_wgrad": ([_P, _L, _P, _L, _L, _P, _I, _I, _P, _P], _I),
+    "mxmoe_ragged_gemm": ([_P, _L, _P, _I, _L, _L, _P, _I, _I, _P, _P, _S, _P], _I),
+    "mxmoe_ragged_workspace_size": ([_L, _L, _L, _I, _I], _S),
+    "mxmoe_ragged_gemm_wgrad": ([_P, _L, _P, _L, _L, _P, _I, _I, _P, _P, _S, _P], _I),
     "mxfp8_swiglu_ckpt": ([_P, _L, _L, _P, _I, _P, _P, _P, _P], _I),
     "mxfp8_swiglu_ckpt_bwd": ([_P, _P, _P, _L, _L, _P, _I, _P, _P, _P], _I),
     "mxfp4_quantize": ([_P, _L, _L, _L, _I, _I, _P, _P, _P], _I),
@@ -656,13 +657,32 @@ def _call(fn, ref, *args):
             _check(fn(*args, _raw_stream(i)))
 
 
-def mxmoe_ragged_gemm(a, w, offsets, transpose_w=False, out=None):
+@functools.lru_cache(maxsize=4096)
+def ragged_workspace_bytes(M, N, K, E, which):
+    """Workspace of a ragged product (which: 0 forward, 1 transpose_w, 2 weight gradient); 0 where it is not split."""
+    return int(lib().mxmoe_ragged_workspace_size(M, N, K, E, which))
+
+
+def _ragged_ws(workspace, ref, M, N, K, E, which):
+    """(address, bytes) of the caller's workspace or of a new one where the product is to be split, and the tensor."""
+    if workspace is None:
+        n = ragged_workspace_bytes(M, N, K, E, which)
+        if n == 0:
+            return None, 0, None
+        workspace = ref.new_empty((n,), dtype=torch.uint8)
+    else:
+        _like(workspace, ref, None, torch.uint8, "workspace")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def mxmoe_ragged_gemm(a, w, offsets, transpose_w=False, out=None, workspace=None):
     """Grouped product over ragged segments (bf16 or fp16, no padding).
 
     a [M, K], w [E, N, K], offsets int32 [E + 1] on the device:
     out[m] = a[m] . w[e]^T for offsets[e] <= m < offsets[e + 1], [M, N].
     transpose_w=True is its input gradient: a [M, N], out[m] = a[m] . w[e], [M, K].
     Rows at or past offsets[E] are not written (a fresh out holds arbitrary values there).
+    workspace (optional): uint8, ragged_workspace_bytes(M, N, K, E, transpose_w) long; calls that may overlap need one each.
     """
     dt = _dtype(a, "a")
     if a.dim() != 2:
@@ -674,15 +694,16 @@ def mxmoe_ragged_gemm(a, w, offsets, transpose_w=False, out=None):
         raise ValueError(f"w must be [E={E}, N, K] with {'N' if transpose_w else 'K'}={a.shape[1]}, got {tuple(w.shape)}")
     M, (_, N, K) = a.shape[0], w.shape
     out = _out(out, a, (M, K if transpose_w else N), a.dtype, "out")
-    _call(lib().mxmoe_ragged_gemm, a, a.data_ptr(), M, w.data_ptr(), E, N, K, offsets.data_ptr(), int(bool(transpose_w)),
-          dt, out.data_ptr())
+    tr = int(bool(transpose_w))
+    ws, n, _keep = _ragged_ws(workspace, a, M, N, K, E, tr)
+    _call(lib().mxmoe_ragged_gemm, a, a.data_ptr(), M, w.data_ptr(), E, N, K, offsets.data_ptr(), tr, dt, out.data_ptr(), ws, n)
     return out
 
 
-def mxmoe_ragged_gemm_wgrad(g, a, offsets, out=None):
+def mxmoe_ragged_gemm_wgrad(g, a, offsets, out=None, workspace=None):
     """Weight gradient of mxmoe_ragged_gemm: g [M, N], a [M, K] -> dw [E, N, K], dw[e] = g_e^T . a_e.
 
-    An expert without rows gets exact zeros."""
+    An expert without rows gets exact zeros.  workspace as mxmoe_ragged_gemm's, with 2 for transpose_w."""
     dt = _dtype(g, "g")
     _like(a, g, None, g.dtype, "a")
     _like(offsets, g, None, torch.int32, "offsets")
@@ -692,8 +713,9 @@ def mxmoe_ragged_gemm_wgrad(g, a, offsets, out=None):
     K = a.shape[1]
     E = offsets.numel() - 1
     out = _out(out, g, (E, N, K), g.dtype, "out")
-    _call(lib().mxmoe_ragged_gemm_wgrad, g, g.data_ptr(), N, a.data_ptr(), K, M, offsets.data_ptr(), E, dt,
-          out.data_ptr())
+    ws, n, _keep = _ragged_ws(workspace, g, M, N, K, E, 2)
+    _call(lib().mxmoe_ragged_gemm_wgrad, g, g.data_ptr(), N, a.data_ptr(), K, M, offsets.data_ptr(), E, dt, out.data_ptr(),
+          ws, n)
     return out
 
 

@@ -26,6 +26,9 @@
 
 namespace mxmoe {
 
+using sm100::launch_dependents;
+using sm100::wait_dependency;
+
 constexpr int kFp4Plain = 0, kFp4Tile = 1, kFp4TileGated = 2;
 
 // Two fp32 -> two E2M1 codes (nearest even, saturating), a in the low bits.
@@ -225,11 +228,6 @@ __host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S, in
   // ring, partial sums (two tiles), f16 activations, then counts, slot order, groups
   return int(kMvWarps * kMvRing * kMvSlot + 2 * kMvWarps * 512 + int64_t(group) * K * 2 * pieces + 64 + (E + 1) * 4 + (4 * S + 1) * 4 + 256);
 }
-
-// Programmatic dependent launch: the next launch of the stream may start its
-// blocks as this grid's leave; it waits for all of this grid's results itself.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

@@ -1,10 +1,19 @@
-// The two 16-bit float types of the ragged, checkpoint and 4-bit operators,
-// as packed pairs (low half first).
+// What the ragged, checkpoint and 4-bit operators share: the two 16-bit float
+// types as packed pairs (low half first), and dependent launches.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "mx_common.cuh"
+
+namespace mxmoe::sm100 {
+
+// Programmatic dependent launch: the next launch of the stream may start its
+// blocks as this grid's leave; it waits for all of this grid's results itself.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace mxmoe::sm100
 
 namespace mxmoe {
 

@@ -24,7 +24,67 @@ int ensure_smem(K kern, std::atomic<uint64_t>& done, int bytes) {
   return MXMOE_OK;
 }
 
+// A launch that may start while the one before it in the stream drains
+// (`after`: that one is this call's own and announced it).
+template <typename K, typename... A>
+cudaError_t launch_after(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool after, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---------------------------------------------------------------- ragged products
+constexpr size_t kRaggedHeader = 256;   // of the workspace: join_kernel's flag
+
+// Units that share a tile's contraction (1: no split): few tiles leave pairs of
+// SMs without work.  As many units as there are pairs, each with eight K blocks
+// or more, where the contraction has at least 48 blocks: the join's launch and
+// workspace cost the caller 5 us, and a lone tile takes 4 us and 0.22 us a block.
+// On the GPU, split against not: weight gradient 24 x 704 of 31134 rows (3 tiles
+// of 487 blocks) 23 / 141 us, forward 128 rows x 2048 x 7168 (8 tiles of 112)
+// 15.5 / 28.8, one row x 4096 x 4096 (16 of 64) 12.4 / 17.9; with 32 blocks the
+// calls take 13.7 us split and 11.4 not.
+int ragged_splits(int64_t tiles, int64_t blocks) {
+  constexpr int64_t pairs = 74;          // of a B200: the size must not depend on the device that is current
+  if (blocks < 48) return 1;
+  return int(std::max<int64_t>(1, std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), blocks / 8)));
+}
+int64_t ragged_tiles(int64_t M, int64_t N, int64_t K, int E, int which) {
+  using C = ragged::Cfg;
+  const int64_t rt = ((which == 1 ? K : N) + C::BM - 1) / C::BM;
+  // every segment's last tile may be short
+  return which == 2 ? int64_t(E) * rt * ((K + C::BN - 1) / C::BN) : (M / C::BN + std::min<int64_t>(E, M)) * rt;
+}
+int64_t ragged_blocks(int64_t M, int64_t N, int64_t K, int which) {
+  return ((which == 0 ? K : which == 1 ? N : M) + ragged::kBK - 1) / ragged::kBK;
+}
+int64_t ragged_values(int64_t M, int64_t N, int64_t K, int E, int which) {
+  return which == 2 ? int64_t(E) * N * K : M * (which == 1 ? K : N);
+}
+
+// A workspace (may be NULL) of the size for this call lets the product be
+// split; without one it runs unsplit.
+int ragged_workspace(ragged::Params* p, int64_t M, int64_t N, int64_t K, int E, int which, void* workspace,
+                     size_t bytes) {
+  p->splits = 1;
+  const size_t need = mxmoe_ragged_workspace_size(M, N, K, E, which);
+  if (!workspace || need == 0) return MXMOE_OK;
+  if (bytes < need) return fail(MXMOE_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", bytes, need);
+  if (!aligned16(workspace)) return fail(MXMOE_ERR_ALIGN, "workspace is not 16-byte aligned");
+  p->splits = ragged_splits(ragged_tiles(M, N, K, E, which), ragged_blocks(M, N, K, which));
+  p->ok = static_cast<int*>(workspace);
+  p->sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRaggedHeader);
+  return MXMOE_OK;
+}
+
 // 16-bit map of rank 2 or 3 ([z,] y, x), dense rows.
 int make_map16(CUtensorMap* map, int dtype, const void* base, int rank, int64_t x, int64_t y, int64_t z, uint32_t bx,
                uint32_t by, CUtensorMapSwizzle swizzle, const char* what) {
@@ -47,6 +107,7 @@ int launch_ragged_dt(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
   static std::atomic<uint64_t> done{0};
   auto kern = ragged::ragged_gemm_kernel<kMode, kDt>;
   MX_TRY(ensure_smem(kern, done, ragged::Cfg::SMEM_BYTES));
+  max_tiles *= p.splits;
   if (max_tiles > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "%lld tiles: too large", (long long)max_tiles);
   // clusters of two CTAs, as many as can be resident
   cudaLaunchConfig_t cfg = {};
@@ -62,6 +123,12 @@ int launch_ragged_dt(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(max_tiles, d->sms / 2)), 1, 1);
   MX_CHECK_CUDA(cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, p), "ragged product launch");
+  if (p.splits > 1) {
+    constexpr bool kW = kMode == ragged::kWgrad;
+    const int64_t values = int64_t(p.rows) * (kW ? int64_t(p.cols) * p.E : p.M);
+    MX_CHECK_CUDA(launch_after(ragged::join_kernel<kW, kDt>, dim3(unsigned((values / 8 + 255) / 256)), 256, 0, stream, true, p),
+                  "ragged join launch");
+  }
   MX_CHECK_CUDA(cudaGetLastError(), "ragged product launch");
   return MXMOE_OK;
 }
@@ -92,23 +159,6 @@ int mv_group(int64_t K, int E, int S, int pieces) {
   for (int g = 8; g >= 1; g >>= 1)
     if (mv_smem(K, g, E, S, pieces) <= 232448 - 1024) return g;
   return 0;
-}
-
-// A launch that may start while the one before it in the stream drains
-// (`after`: that one is this call's own and announced it).
-template <typename K, typename... A>
-cudaError_t launch_after(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, bool after, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int kDt, bool kGated, int kOut>
@@ -174,14 +224,21 @@ size_t carve_decode(uint8_t* base, int64_t S, int64_t D, int64_t F, DecodeWs* w)
 
 extern "C" {
 
+size_t mxmoe_ragged_workspace_size(int64_t M, int64_t N, int64_t K, int E, int which) {
+  if (M <= 0 || N <= 0 || K <= 0 || E <= 0 || which < 0 || which > 2 || N >= (int64_t(1) << 30) || K >= (int64_t(1) << 30) ||
+      M > (int64_t(1) << 31))
+    return 0;
+  const int splits = ragged_splits(ragged_tiles(M, N, K, E, which), ragged_blocks(M, N, K, which));
+  return splits > 1 ? kRaggedHeader + size_t(splits) * ragged_values(M, N, K, E, which) * 4 : 0;
+}
+
 int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N, int64_t K,
-                      const int32_t* expert_offsets, int transpose_w, int dtype, void* out, cudaStream_t stream) {
+                      const int32_t* expert_offsets, int transpose_w, int dtype, void* out, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
   MX_TRY(check_ragged(M, N, K, E, expert_offsets, dtype));
   if (transpose_w != 0 && transpose_w != 1) return fail(MXMOE_ERR_ARG, "transpose_w=%d must be 0 or 1", transpose_w);
   if (M == 0) return MXMOE_OK;
   MX_TRY(check_ptrs({{"a", a}, {"w", w}, {"out", out}}));
-  DevInfo* d;
-  MX_TRY(device_info(&d));
   ragged::Params p{};
   p.E = E;
   p.M = M;
@@ -189,17 +246,20 @@ int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N,
   p.out = static_cast<uint16_t*>(out);
   p.rows = int(transpose_w ? K : N);
   p.kext = int(transpose_w ? N : K);
+  MX_TRY(ragged_workspace(&p, M, N, K, E, transpose_w, workspace, workspace_bytes));
+  DevInfo* d;
+  MX_TRY(device_info(&d));
   CUtensorMap ma, mb;
   MX_TRY(make_map16(&ma, dtype, w, 3, K, N, E, 64, transpose_w ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B, "weights"));
   MX_TRY(make_map16(&mb, dtype, a, 2, p.kext, M, 1, 64, ragged::Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
-  // every segment's last tile may be short
-  const int64_t tiles = (M / ragged::Cfg::BN + std::min<int64_t>(E, M)) * ((p.rows + ragged::Cfg::BM - 1) / ragged::Cfg::BM);
+  const int64_t tiles = ragged_tiles(M, N, K, E, transpose_w);
   return transpose_w ? launch_ragged<ragged::kDgrad>(dtype, ma, mb, mb, p, tiles, d, stream)
                      : launch_ragged<ragged::kFwd>(dtype, ma, mb, mb, p, tiles, d, stream);
 }
 
 int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, int64_t M,
-                            const int32_t* expert_offsets, int E, int dtype, void* dw, cudaStream_t stream) {
+                            const int32_t* expert_offsets, int E, int dtype, void* dw, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
   MX_TRY(check_ragged(M, N, K, E, expert_offsets, dtype));
   MX_TRY(check_ptrs({{"dw", dw}}));
   DevInfo* d;
@@ -209,18 +269,20 @@ int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, 
     return MXMOE_OK;
   }
   MX_TRY(check_ptrs({{"g", g}, {"a", a}}));
-  MX_TRY(device_info(&d));
   ragged::Params p{};
   p.E = E;
   p.M = M;
   p.offsets = expert_offsets;
   p.rows = int(N);
   p.cols = int(K);
+  p.out = static_cast<uint16_t*>(dw);
+  MX_TRY(ragged_workspace(&p, M, N, K, E, 2, workspace, workspace_bytes));
+  MX_TRY(device_info(&d));
   CUtensorMap ma, mb, mo;
   MX_TRY(make_map16(&ma, dtype, g, 2, N, M, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "gradients"));
   MX_TRY(make_map16(&mb, dtype, a, 2, K, M, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
   MX_TRY(make_map16(&mo, dtype, dw, 3, K, N, E, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "weight gradients"));
-  const int64_t tiles = int64_t(E) * ((N + ragged::Cfg::BM - 1) / ragged::Cfg::BM) * ((K + ragged::Cfg::BN - 1) / ragged::Cfg::BN);
+  const int64_t tiles = ragged_tiles(M, N, K, E, 2);
   return launch_ragged<ragged::kWgrad>(dtype, ma, mb, mo, p, tiles, d, stream);
 }
 

@@ -54,8 +54,17 @@ struct Params {
   int cols;                  // kWgrad: N-side extent (K); else unused
   int kext;                  // contraction extent (kFwd K, kDgrad N; kWgrad: per segment)
   const int32_t* offsets;
-  uint16_t* out;             // kFwd / kDgrad: [M, rows]
+  uint16_t* out;             // kFwd / kDgrad: [M, rows]; kWgrad (for join_kernel): [E, rows, cols]
+  // Few tiles with a long contraction: a tile's K blocks go to `splits` units,
+  // which leave fp32 sums for join_kernel.
+  int splits;                // 1: no split
+  int* ok;                   // set when the offsets are good, for join_kernel
+  float* sums;               // [splits][M, rows] (kWgrad: [splits][E, rows, cols])
 };
+
+// Units that share a tile of nk K blocks: at least kMinBlocks each.
+constexpr int kMinBlocks = 4;
+__host__ __device__ inline int parts_of(int nk, int splits) { return max(1, min(splits, nk / kMinBlocks)); }
 
 struct Cfg {
   static constexpr int BM = 256, BN = 256;                            // of the pair
@@ -128,7 +137,9 @@ struct Walk {
 
 struct Tile {
   int e;
-  int nk;       // K blocks
+  int nk;       // K blocks of the tile
+  int kb0, kb1; // this unit's
+  int part;
   int r0;       // first M-side row (of the expert's matrix)
   int n;        // N-side columns (tokens; kWgrad: columns of K)
   int t0;       // first token (kFwd / kDgrad: of the tile; kWgrad: of the segment)
@@ -148,6 +159,11 @@ template <int kMode>
 __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, const int32_t* tab, const uint16_t* ord,
                                          uint32_t t) {
   Tile T;
+  T.part = 0;
+  if (p.splits > 1) {
+    T.part = int(t % uint32_t(p.splits));
+    t /= uint32_t(p.splits);
+  }
   const uint32_t rt = uint32_t(p.rows + Cfg::BM - 1) / Cfg::BM;
   if constexpr (kMode == kWgrad) {
     const uint32_t ct = uint32_t(p.cols + Cfg::BN - 1) / Cfg::BN;
@@ -179,6 +195,13 @@ __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, c
     T.nk = (p.kext + kBK - 1) / kBK;
     T.c0 = 0;
     T.len = 0;
+  }
+  T.kb0 = 0;
+  T.kb1 = T.nk;
+  if (p.splits > 1) {
+    const int parts = parts_of(T.nk, p.splits);
+    T.kb0 = T.part < parts ? int(int64_t(T.nk) * T.part / parts) : 0;
+    T.kb1 = T.part < parts ? int(int64_t(T.nk) * (T.part + 1) / parts) : 0;
   }
   return T;
 }
@@ -214,7 +237,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     const int32_t o = offs[i];
     if (o < 0 || int64_t(o) > p.M || (i == 0 && o != 0) || (i < p.E && offs[i + 1] < o)) bad = true;
   }
-  if (__syncthreads_or(bad)) {
+  bad = __syncthreads_or(bad);
+  if (p.splits > 1) {
+    launch_dependents();
+    if (threadIdx.x == 0 && blockIdx.x == 0) *p.ok = !bad;
+  }
+  if (bad) {
     if (threadIdx.x == 0 && blockIdx.x == 0) raise_device_error(kErrOffsets);
     return;
   }
@@ -277,7 +305,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   tc_fence_after();
   const uint32_t tmem_base = misc[0];
   const int rt = (p.rows + C::BM - 1) / C::BM;
-  const uint32_t ntiles = uint32_t(kMode == kWgrad ? p.E * ((p.cols + C::BN - 1) / C::BN) : tab[p.E]) * rt;
+  const uint32_t ntiles = uint32_t(kMode == kWgrad ? p.E * ((p.cols + C::BN - 1) / C::BN) : tab[p.E]) * rt * p.splits;
 
   if (warp == 0) {
     // ================= producer (each CTA loads its own operand halves; the
@@ -292,7 +320,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const int boxes = (half + kCols - 1) / kCols;
       const uint32_t bytes = C::A_BYTES + boxes * kCols * 128;       // per CTA
       const int r0 = T.r0 + rank * 128, b0 = rank * half;
-      for (int kb = 0; kb < T.nk; ++kb) {
+      for (int kb = T.kb0; kb < T.kb1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1))) { ok = false; break; }
         if (elect_one()) {
           const uint32_t as = sbase + C::OFF_A + stage * C::A_BYTES, bs = sbase + C::OFF_B + stage * C::B_BYTES;
@@ -347,7 +375,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next()) {
         const Tile T = next;
         const bool more = w.after() < ntiles;
-        if (T.nk == 0) {
+        if (T.kb1 == T.kb0) {
           if (more) next = get_tile<kMode>(p, offs, tab, ord, w.after());
           continue;
         }
@@ -355,7 +383,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::BN;
         const uint32_t idesc = f16_idesc(kDt == kBF16 ? 1 : 0, kAMn, kBMn, C::BM, uint32_t((T.n + 15) & ~15));
-        for (int kb = 0; kb < T.nk; ++kb) {
+        for (int kb = T.kb0; kb < T.kb1; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait_cluster(full_bar(stage), phase))) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
@@ -363,12 +391,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             const int steps = kMode == kWgrad ? min(kBK / 16, (T.len - kb * kBK + 15) >> 4) : kBK / 16;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-              if (kMode != kWgrad || k < steps) mma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+              if (kMode != kWgrad || k < steps) mma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, kb != T.kb0 || k != 0);
             mma_commit_pair(empty_bar(stage));
-            if (kb == T.nk - 1) mma_commit_pair(tfull_bar(acc));
+            if (kb == T.kb1 - 1) mma_commit_pair(tfull_bar(acc));
           }
           __syncwarp();
-          if (more && kb == min(2, T.nk - 1)) next = get_tile<kMode>(p, offs, tab, ord, w.after());
+          if (more && kb == min(T.kb0 + 2, T.kb1 - 1)) next = get_tile<kMode>(p, offs, tab, ord, w.after());
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         }
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -383,9 +411,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       bool ok = true;
       for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next()) {
         const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
-        if (T.nk == 0) continue;
-        stage = (stage + T.nk - 1) % C::kStages;                     // the segment's last block
-        const int rem = T.len - (T.nk - 1) * kBK;
+        if (T.kb1 == T.kb0) continue;
+        stage = (stage + T.kb1 - T.kb0 - 1) % C::kStages;            // this unit's last block
+        const int rem = T.len - (T.kb1 - 1) * kBK;
         if (rem < kBK && (rem & 15)) {
           ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(stage), (used >> stage) & 1));
           if (!ok) break;
@@ -424,7 +452,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
       const int row = T.r0 + rank * 128 + q * 32;                // this warp's 32 M-side rows
       const int chunks = (T.n + 31) >> 5;
-      const bool any = T.nk != 0;                                // kWgrad: an expert without rows has a zero gradient
+      const bool any = T.kb1 != T.kb0;                           // kWgrad: an expert without rows has a zero gradient
+      if (!any && p.splits > 1) continue;                        // (join_kernel writes it)
       if (any) {
         if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase))) {
           if (lane == 0) raise_device_error(kErrTimeout);
@@ -440,6 +469,25 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+        if (p.splits > 1) {
+          // fp32 sums as they lie: kWgrad 32 columns of a row per lane, else a
+          // column per lane
+          if (row + lane < p.rows) {
+            if constexpr (kMode == kWgrad) {
+              float* dst = p.sums + ((int64_t(T.part) * p.E + T.e) * p.rows + row + lane) * p.cols + T.c0 + 32 * c;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (32 * c + j < T.n)                              // (columns are a multiple of 8)
+                  *reinterpret_cast<uint4*>(dst + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+            } else {
+              float* dst = p.sums + (int64_t(T.part) * p.M + T.t0 + 32 * c) * p.rows + row + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * c + j < T.n) dst[int64_t(j) * p.rows] = __uint_as_float(r[j]);
+            }
+          }
+          continue;
         }
         if constexpr (kMode == kWgrad) {
           // one row of 32 columns per lane: staged in the store map's 64-byte
@@ -505,6 +553,38 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
   }
+}
+
+// The units' sums of a split product, added in order and rounded once.
+// kWgrad: parts by the expert's rows, zeros for an expert without; else rows
+// below offsets[E].  Eight neighbouring values a thread.
+template <bool kW, int kDt>
+__global__ void __launch_bounds__(256) join_kernel(const Params p) {
+  wait_dependency();
+  if (!*p.ok) return;
+  const int64_t each = int64_t(p.rows) * (kW ? p.cols : 1);          // values of an expert's matrix, of a row
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8, total = each * (kW ? int64_t(p.E) : p.M);
+  const int64_t live = kW ? total : each * p.offsets[p.E];
+  if (i >= live) return;
+  int parts;
+  if constexpr (kW) {
+    const int e = int(i / each), len = p.offsets[e + 1] - p.offsets[e];
+    parts = len == 0 ? 0 : parts_of((len + kBK - 1) / kBK, p.splits);
+  } else {
+    parts = parts_of((p.kext + kBK - 1) / kBK, p.splits);
+  }
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll 4
+  for (int q = 0; q < parts; ++q) {
+    const float4* s = reinterpret_cast<const float4*>(p.sums + q * total + i);
+    const float4 a = s[0], b = s[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  *reinterpret_cast<uint4*>(p.out + i) = make_uint4(pack16x2<kDt>(v[0], v[1]), pack16x2<kDt>(v[2], v[3]),
+                                                    pack16x2<kDt>(v[4], v[5]), pack16x2<kDt>(v[6], v[7]));
 }
 
 }  // namespace mxmoe::ragged

@@ -23,11 +23,11 @@ def _err(L):
 
 
 def test_ragged_refusals(L):
-    ok = dict(a=FAKE, M=10, w=FAKE, E=2, N=16, K=24, off=FAKE, tr=0, dt=0, out=FAKE)
+    ok = dict(a=FAKE, M=10, w=FAKE, E=2, N=16, K=24, off=FAKE, tr=0, dt=0, out=FAKE, ws=None, n=0)
 
     def call(**kw):
         v = {**ok, **kw}
-        return L.mxmoe_ragged_gemm(v["a"], v["M"], v["w"], v["E"], v["N"], v["K"], v["off"], v["tr"], v["dt"], v["out"], None)
+        return L.mxmoe_ragged_gemm(v["a"], v["M"], v["w"], v["E"], v["N"], v["K"], v["off"], v["tr"], v["dt"], v["out"], v["ws"], v["n"], None)
 
     for kw, status, word in ((dict(N=12), 2, "N=12"), (dict(K=0), 2, "K=0"), (dict(M=-1), 2, "M=-1"), (dict(M=(1 << 31) - 1023), 2, "M="),
                              (dict(E=0), 2, "E=0"), (dict(E=1025), 2, "E=1025"), (dict(off=None), 1, "expert_offsets"),
@@ -37,12 +37,29 @@ def test_ragged_refusals(L):
     assert call(M=0) == 0                                          # nothing to do, nothing touched
 
 
+def test_ragged_workspace_arithmetic(L):
+    f = L.mxmoe_ragged_workspace_size
+    assert f(49152, 2816, 2048, 64, 0) == 0 and f(49152, 2816, 2048, 64, 2) == 0        # tiles enough
+    assert f(10, 16, 24, 2, 0) == 0 and f(64, 16, 24, 1, 2) == 0                          # a short contraction
+    assert f(128, 2048, 7168, 1, 0) == 256 + 9 * 128 * 2048 * 4                           # 8 tiles: 74 / 8 units each
+    assert f(128, 2048, 7168, 1, 1) == 0                                                  # 32 blocks: not worth a launch
+    assert f(128, 4096, 7168, 1, 1) == 256 + 2 * 128 * 7168 * 4                           # 28 tiles, 64 blocks
+    assert f(31134, 24, 704, 1, 2) == 256 + 24 * 24 * 704 * 4                             # 3 tiles, 487 blocks
+    s = L.mxmoe_ragged_gemm(FAKE, 128, FAKE, 1, 2048, 7168, FAKE, 0, 0, FAKE, FAKE, 1000, None)
+    assert s == 8 and "workspace of 1000 bytes" in _err(L)
+    s = L.mxmoe_ragged_gemm(FAKE, 128, FAKE, 1, 2048, 7168, FAKE, 0, 0, FAKE, MIS, 1 << 30, None)
+    assert s == 3 and "workspace is not" in _err(L)
+    s = L.mxmoe_ragged_gemm_wgrad(FAKE, 24, FAKE, 704, 31134, FAKE, 1, 0, FAKE, FAKE, 1000, None)
+    assert s == 8
+    assert f(0, 16, 24, 1, 0) == 0 and f(10, 16, 24, 0, 0) == 0 and f(10, 16, 24, 1, 3) == 0
+
+
 def test_ragged_wgrad_refusals(L):
     ok = dict(g=FAKE, N=16, a=FAKE, K=24, M=10, off=FAKE, E=2, dt=1, out=FAKE)
 
     def call(**kw):
         v = {**ok, **kw}
-        return L.mxmoe_ragged_gemm_wgrad(v["g"], v["N"], v["a"], v["K"], v["M"], v["off"], v["E"], v["dt"], v["out"], None)
+        return L.mxmoe_ragged_gemm_wgrad(v["g"], v["N"], v["a"], v["K"], v["M"], v["off"], v["E"], v["dt"], v["out"], None, 0, None)
 
     for kw, status, word in ((dict(N=4), 2, "N=4"), (dict(K=28), 2, "K=28"), (dict(E=-3), 2, "E=-3"), (dict(off=None), 1, "expert_offsets"),
                              (dict(g=None), 1, "g is NULL"), (dict(a=MIS), 3, "a is not"), (dict(out=None), 1, "dw is NULL"), (dict(dt=-1), 9, "dtype=-1")):

@@ -221,3 +221,83 @@ def test_repeats_are_bitwise_equal():
     for _ in range(3):
         again = (mxk.mxmoe_ragged_gemm(a, w, off), mxk.mxmoe_ragged_gemm_wgrad(d, a, off))
         assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+# ------------------------------------------------------------------------------------------------ split contractions
+SPLIT = [  # segment lengths, N, K, which of (forward, input gradient, weight gradient) are split
+    ([70, 0, 13], 40, 4104, (0,)),
+    ([5], 4104, 264, (1,)),
+    ([0, 3001, 0, 130, 77], 24, 72, (2,)),
+    ([3100, 1], 136, 264, (2,)),
+    ([300], 264, 3080, (0,)),
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("lens,N,K,which", SPLIT)
+def test_split_whole_numbers_are_exact(lens, N, K, which, dt):
+    """Few tiles with a long contraction: units share a tile and a second launch joins their sums."""
+    g = np.random.default_rng(11)
+    off = P.offsets_of(lens)
+    R, E, tail = sum(lens), len(lens), 3
+    M = R + tail
+    a, gr, w = _ints(g, M, K, top=1), _ints(g, M, N, top=1), _ints(g, E, N, K, top=1)
+    d = [t.to(DEV, dt) for t in (a, gr, w)]
+    for k in (0, 1, 2):
+        assert (mxk.ragged_workspace_bytes(M, N, K, E, k) > 0) or k not in which, k
+    for tr, x in ((False, 0), (True, 1)):
+        out = torch.full((M, K if tr else N), 7.0, dtype=dt, device=DEV)
+        mxk.mxmoe_ragged_gemm(d[x], d[2], off.to(DEV), transpose_w=tr, out=out)
+        ref, _ = P.ragged(gr if tr else a, w, off, tr)
+        ref[R:] = 7.0
+        P.assert_same(out, _round(ref, dt), f"out, transpose_w={tr}")
+    dw = mxk.mxmoe_ragged_gemm_wgrad(d[1], d[0], off.to(DEV), out=torch.full((E, N, K), float("nan"), dtype=dt, device=DEV))
+    P.assert_same(dw, _round(P.wgrad(gr, a, off)[0], dt), "dw")
+    assert mxk.device_error() == 0
+
+
+def test_split_bad_table_writes_nothing():
+    off = torch.tensor([0, 9000], dtype=torch.int32, device=DEV)
+    a, g = torch.ones(4000, 72, dtype=BF, device=DEV), torch.ones(4000, 24, dtype=BF, device=DEV)
+    assert mxk.ragged_workspace_bytes(4000, 24, 72, 1, 2) > 0
+    dw = torch.full((1, 24, 72), 3.0, dtype=BF, device=DEV)
+    mxk.mxmoe_ragged_gemm_wgrad(g, a, off, out=dw)
+    assert mxk.device_error() == 4 and (dw == 3).all()
+
+
+def test_split_captured_with_a_workspace_each():
+    """Two graphs with their own workspaces on two streams at once; the split and the unsplit product on whole numbers agree."""
+    r = np.random.default_rng(12)
+    jobs = []
+    for _ in range(2):
+        a, g = _ints(r, 5000, 72, top=1).to(DEV, BF), _ints(r, 5000, 24, top=1).to(DEV, BF)
+        off = P.offsets_of([4000, 1000]).to(DEV)
+        ws = torch.empty(mxk.ragged_workspace_bytes(5000, 24, 72, 2, 2), dtype=torch.uint8, device=DEV)
+        out = torch.empty(2, 24, 72, dtype=BF, device=DEV)
+        run = lambda a=a, g=g, off=off, ws=ws, out=out: mxk.mxmoe_ragged_gemm_wgrad(g, a, off, out=out, workspace=ws)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        off.copy_(P.offsets_of([1, 4500]))
+        a.copy_(_ints(r, 5000, 72, top=1))
+        jobs.append((graph, torch.cuda.Stream(), a, g, off, out))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, s, *_ in jobs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, a, g, off, out in jobs:
+        P.assert_same(out, _round(P.wgrad(g.cpu(), a.cpu(), off.cpu())[0], BF), "dw")
+
+
+def test_split_normal_values_within_the_bound():
+    g = torch.Generator().manual_seed(13)
+    lens, N, K = [4000, 0, 500], 40, 136
+    off = P.offsets_of(lens)
+    a, gr = torch.randn(4500, K, generator=g).to(BF), torch.randn(4500, N, generator=g).to(BF)
+    ref, mag = P.wgrad(gr, a, off)
+    s = max(lens) * 2.0 ** -23 * mag
+    P.assert_within(mxk.mxmoe_ragged_gemm_wgrad(gr.to(DEV), a.to(DEV), off.to(DEV)), ref, P.u(BF) * (ref.abs() + s) + s + P.tiny(BF), "dw")
