@@ -515,24 +515,39 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         } else {
           // lane = output column, register = token: transposed through shared
           // memory (a token's 32 columns are one 64-byte line, written two
-          // bytes a lane without conflicts), then 16-byte stores of four
-          // lanes a token
+          // bytes a lane without conflicts).  A chunk of 32 tokens leaves by
+          // TMA (64-byte swizzle: piece j of line t at j ^ ((t >> 1) & 3); the
+          // map clips the columns), the segment's last tokens by 16-byte stores
+          // of four lanes a token
+          const bool whole = 32 * c + 32 <= T.n;
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint32_t w = pack16x2<kDt>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            *reinterpret_cast<uint16_t*>(sbuf + (2 * j) * 64 + lane * 2) = uint16_t(w & 0xFFFFu);
-            *reinterpret_cast<uint16_t*>(sbuf + (2 * j + 1) * 64 + lane * 2) = uint16_t(w >> 16);
+            uint8_t* line = sbuf + (2 * j) * 64 + (((lane >> 3) ^ (j & 3)) << 4) + (lane & 7) * 2;
+            *reinterpret_cast<uint16_t*>(line) = uint16_t(w & 0xFFFFu);
+            *reinterpret_cast<uint16_t*>(line + 64) = uint16_t(w >> 16);
           }
-          __syncwarp();
-          const int col = row + (lane & 3) * 8;
+          if (whole) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && row < p.rows) {
+              tma_store_2d(&tmap_o, smem_u32(sbuf), row, T.t0 + 32 * c);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            const int col = row + (lane & 3) * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = 8 * i + (lane >> 2);
-            const uint4 v = *reinterpret_cast<const uint4*>(sbuf + tok * 64 + (lane & 3) * 16);
-            if (32 * c + tok < T.n && col < p.rows)
-              *reinterpret_cast<uint4*>(p.out + int64_t(T.t0 + 32 * c + tok) * p.rows + col) = v;
+            for (int i = 0; i < 4; ++i) {
+              const int tok = 8 * i + (lane >> 2);
+              const uint4 v = *reinterpret_cast<const uint4*>(sbuf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
+              if (32 * c + tok < T.n && col < p.rows)
+                *reinterpret_cast<uint4*>(p.out + int64_t(T.t0 + 32 * c + tok) * p.rows + col) = v;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (any) {
@@ -542,7 +557,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
     }
-    if (kMode == kWgrad && lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   // ---- teardown: every role has left its loop (all waits are bounded); neither
   // CTA frees its TMEM or leaves while the other may still arrive on its
