@@ -644,7 +644,8 @@ def _like(t, ref, shape, dtype, name: str):
 
 def _out(t, ref, shape, dtype, name: str):
     """An output: the caller's, checked, or a new one on ref's device."""
-    return ref.new_empty(shape, dtype=dtype) if t is None else _like(t, ref, shape, dtype, name)
+    # (sizes as arguments: 0.4 us less than a tuple or new_empty)
+    return torch.empty(*shape, dtype=dtype, device=ref.device) if t is None else _like(t, ref, shape, dtype, name)
 
 
 def _call(fn, ref, *args):
@@ -669,7 +670,7 @@ def _ragged_ws(workspace, ref, M, N, K, E, which):
         n = ragged_workspace_bytes(M, N, K, E, which)
         if n == 0:
             return None, 0, None
-        workspace = ref.new_empty((n,), dtype=torch.uint8)
+        workspace = torch.empty(n, dtype=torch.uint8, device=ref.device)
     else:
         _like(workspace, ref, None, torch.uint8, "workspace")
     return workspace.data_ptr(), workspace.numel(), workspace
@@ -769,8 +770,8 @@ def mxfp4_quantize(w, layout: int = PLAIN):
         raise ValueError("w must be 2-D or 3-D")
     E = w.shape[0] if w.dim() == 3 else 1
     rows, cols = w.shape[-2], w.shape[-1]
-    codes = _u8((*w.shape[:-1], cols // 2), w.device)
-    scales = _u8((*w.shape[:-1], cols // 32), w.device)
+    codes = _out(None, w, (*w.shape[:-1], cols // 2), torch.uint8, "codes")
+    scales = _out(None, w, (*w.shape[:-1], cols // 32), torch.uint8, "scales")
     _call(lib().mxfp4_quantize, w, w.data_ptr(), E, rows, cols, dt, layout, codes.data_ptr(), scales.data_ptr())
     return dict(codes=codes, scales=scales)
 
@@ -785,7 +786,7 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16):
     cols = 2 * codes.shape[-1]
     rows = codes.shape[-2] * (codes.shape[0] if codes.dim() == 3 else 1)
     _like(scales, codes, (*codes.shape[:-1], cols // 32), torch.uint8, "scales")
-    out = torch.empty((*codes.shape[:-1], cols), dtype=dtype, device=codes.device)
+    out = _out(None, codes, (*codes.shape[:-1], cols), dtype, "out")
     _call(lib().mxfp4_dequantize, codes, codes.data_ptr(), scales.data_ptr(), rows, cols, _DTYPES[dtype], out.data_ptr())
     return out
 
@@ -849,7 +850,7 @@ def moe_layer_decode_fp4(x_tokens, topk_ids, topk_weights, qw, out=None, workspa
     _like(qw["w2_scales"], x_tokens, (E, D, F // 32), torch.uint8, "qw['w2_scales']")
     out = _out(out, x_tokens, (T, D), x_tokens.dtype, "out")
     if workspace is None:
-        workspace = x_tokens.new_empty((decode_workspace_bytes(T, k, D, F),), dtype=torch.uint8)
+        workspace = torch.empty(decode_workspace_bytes(T, k, D, F), dtype=torch.uint8, device=x_tokens.device)
     else:
         _like(workspace, x_tokens, None, torch.uint8, "workspace")
     st = _Q4Weights(c13.data_ptr(), qw["w13_scales"].data_ptr(), c2.data_ptr(), qw["w2_scales"].data_ptr())
