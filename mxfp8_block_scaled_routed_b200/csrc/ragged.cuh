@@ -76,11 +76,13 @@ struct Cfg {
   static constexpr int OFF_EPI = OFF_B + kStages * B_BYTES;
   static constexpr int EPI_WARP_BYTES = 2048;  // one 32 x 32 block of 16-bit outputs per warp
   static constexpr int OFF_BAR = OFF_EPI + 8 * EPI_WARP_BYTES;
-  static constexpr int NUM_BARS = 3 * kStages + 4;
+  static constexpr int kInfo = 16;             // tiles that the producer may announce ahead
+  static constexpr int NUM_BARS = 3 * kStages + 4 + 2 * kInfo;
   static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) & ~15;
   // offsets [E + 1]; first token tile of each expert [E + 1] (kWgrad: its rows); kWgrad's schedule order [E]
   static constexpr int TAB = (kMaxE + 4) * 4;
-  static constexpr int OFF_TAB = OFF_MISC + 16;
+  static constexpr int OFF_INFO = OFF_MISC + 16, INFO = 32;
+  static constexpr int OFF_TAB = OFF_INFO + kInfo * INFO;
   static constexpr int SMEM_BYTES = OFF_TAB + 2 * TAB + kMaxE * 2 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(OFF_TAB % 16 == 0 && TAB % 16 == 0, "the tables are read 16 bytes at a time");
@@ -131,15 +133,12 @@ struct Walk {
   __device__ __forceinline__ Walk(uint32_t u, uint32_t n) : unit(u), units(n), base(0), back(0) {}
   __device__ __forceinline__ uint32_t at(uint32_t rev) const { return kMode == kWgrad && rev ? units - 1 - unit : unit; }
   __device__ __forceinline__ uint32_t tile() const { return base + at(back); }
-  __device__ __forceinline__ uint32_t after() const { return base + units + at(back ^ 1); }
   __device__ __forceinline__ void next() { base += units; back ^= 1; }
 };
 
 struct Tile {
-  int e;
-  int nk;       // K blocks of the tile
-  int kb0, kb1; // this unit's
-  int part;
+  int e, part;
+  int kb0, kb1; // this unit's K blocks
   int r0;       // first M-side row (of the expert's matrix)
   int n;        // N-side columns (tokens; kWgrad: columns of K)
   int t0;       // first token (kFwd / kDgrad: of the tile; kWgrad: of the segment)
@@ -159,6 +158,7 @@ template <int kMode>
 __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, const int32_t* tab, const uint16_t* ord,
                                          uint32_t t) {
   Tile T;
+  int nk;       // of the whole tile
   T.part = 0;
   if (p.splits > 1) {
     T.part = int(t % uint32_t(p.splits));
@@ -175,7 +175,7 @@ __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, c
     T.n = min(Cfg::BN, p.cols - T.c0);
     T.t0 = offs[T.e];
     T.len = offs[T.e + 1] - offs[T.e];
-    T.nk = (T.len + kBK - 1) / kBK;
+    nk = (T.len + kBK - 1) / kBK;
   } else {
     int lo = 0, hi = p.E;                      // last expert whose first tile is at or before t
     while (hi - lo > 1) {
@@ -192,16 +192,16 @@ __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, c
     T.r0 = int(blk * kRows + in - j * br) * Cfg::BM;
     T.t0 = offs[T.e] + int(j) * per;
     T.n = min(per, len - int(j) * per);
-    T.nk = (p.kext + kBK - 1) / kBK;
+    nk = (p.kext + kBK - 1) / kBK;
     T.c0 = 0;
     T.len = 0;
   }
   T.kb0 = 0;
-  T.kb1 = T.nk;
+  T.kb1 = nk;
   if (p.splits > 1) {
-    const int parts = parts_of(T.nk, p.splits);
-    T.kb0 = T.part < parts ? int(int64_t(T.nk) * T.part / parts) : 0;
-    T.kb1 = T.part < parts ? int(int64_t(T.nk) * (T.part + 1) / parts) : 0;
+    const int parts = parts_of(nk, p.splits);
+    T.kb0 = T.part < parts ? int(int64_t(nk) * T.part / parts) : 0;
+    T.kb1 = T.part < parts ? int(int64_t(nk) * (T.part + 1) / parts) : 0;
   }
   return T;
 }
@@ -224,6 +224,31 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   auto tail_bar = [&](int s) { return smem_u32(&bars[2 * C::kStages + s]); };
   auto tfull_bar = [&](int a) { return smem_u32(&bars[3 * C::kStages + a]); };
   auto tempty_bar = [&](int a) { return smem_u32(&bars[3 * C::kStages + 2 + a]); };
+  auto info_bar = [&](int s) { return smem_u32(&bars[3 * C::kStages + 4 + s]); };
+  auto seen_bar = [&](int s) { return smem_u32(&bars[3 * C::kStages + 4 + C::kInfo + s]); };
+  // A tile's place takes several hundred cycles to work out (a search, divisions).
+  // The producer does it, tiles ahead, and the other roles of its CTA read it
+  // (their i-th tile; ok: announced in time): 32768 rows x 8 x 4096 x 256 88 -> 82
+  // us against every role on its own, 64 weight gradients of 2048 x 2048 from 6000
+  // rows 119 -> 117.
+  auto read_tile = [&](uint32_t i, bool& ok) {
+    const int s = i % C::kInfo;
+    ok = __all_sync(0xffffffffu, mbar_wait(info_bar(s), (i / C::kInfo) & 1));
+    const uint4 a = lds128(sbase + C::OFF_INFO + s * C::INFO), b = lds128(sbase + C::OFF_INFO + s * C::INFO + 16);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seen_bar(s));
+    Tile T;
+    T.e = int(a.x & 0xFFFFu);
+    T.part = int(a.x >> 16);
+    T.kb0 = int(a.y);
+    T.kb1 = int(a.z);
+    T.r0 = int(a.w);
+    T.n = int(b.x);
+    T.t0 = int(b.y);
+    T.c0 = int(b.z);
+    T.len = int(b.w);
+    return T;
+  };
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   int32_t* offs = reinterpret_cast<int32_t*>(smem + C::OFF_TAB);
   int32_t* tab = offs + C::TAB / 4;
@@ -294,6 +319,10 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 16);                                  // the epilogue warps of both CTAs
     }
+    for (int i = 0; i < C::kInfo; ++i) {
+      mbar_init(info_bar(i), 1);
+      mbar_init(seen_bar(i), 8 + (rank == 0) + (kMode == kWgrad));   // epilogue warps, MMA issuer, kWgrad's warp 3
+    }
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -311,10 +340,19 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     // ================= producer (each CTA loads its own operand halves; the
     // bytes of both are credited to the even CTA's full barrier)
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, at = 0;
     bool ok = true;
-    for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next()) {
+    for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next(), ++at) {
       const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
+      const int slot = at % C::kInfo;
+      if (!__all_sync(0xffffffffu, mbar_wait(seen_bar(slot), ((at / C::kInfo) & 1) ^ 1))) { ok = false; break; }
+      if (elect_one()) {
+        const uint32_t to = sbase + C::OFF_INFO + slot * C::INFO;
+        sts128(to, make_uint4(T.e | T.part << 16, T.kb0, T.kb1, T.r0));
+        sts128(to + 16, make_uint4(T.n, T.t0, T.c0, T.len));
+        mbar_arrive(info_bar(slot));
+      }
+      __syncwarp();
       const int half = ((T.n + 15) & ~15) >> 1;                      // columns of B per CTA
       constexpr int kCols = kMode == kWgrad ? 64 : C::kBox;          // per box
       const int boxes = (half + kCols - 1) / kCols;
@@ -368,17 +406,11 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const uint64_t a_desc = smem_desc(sbase + C::OFF_A, kAMn ? 8192 : 0, 1024, 2);
       const uint64_t b_desc = smem_desc(sbase + C::OFF_B, kBMn ? 8192 : 0, 1024, 2);
       constexpr uint64_t a_step = (kAMn ? 2048 : 32) >> 4, b_step = (kBMn ? 2048 : 32) >> 4;
-      // the next tile's place is worked out between this one's K blocks, beside
-      // MMAs already queued (it takes several hundred cycles)
-      Tile next{};
-      if (unit < ntiles) next = get_tile<kMode>(p, offs, tab, ord, unit);
-      for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next()) {
-        const Tile T = next;
-        const bool more = w.after() < ntiles;
-        if (T.kb1 == T.kb0) {
-          if (more) next = get_tile<kMode>(p, offs, tab, ord, w.after());
-          continue;
-        }
+      uint32_t at = 0;
+      for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next(), ++at) {
+        const Tile T = read_tile(at, ok);
+        if (!ok) break;
+        if (T.kb1 == T.kb0) continue;
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1))) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * C::BN;
@@ -396,7 +428,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             if (kb == T.kb1 - 1) mma_commit_pair(tfull_bar(acc));
           }
           __syncwarp();
-          if (more && kb == min(T.kb0 + 2, T.kb1 - 1)) next = get_tile<kMode>(p, offs, tab, ord, w.after());
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         }
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -407,10 +438,11 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     // ================= kWgrad: clear this CTA's rows past a segment's end
     if constexpr (kMode == kWgrad) {
       int stage = 0;
-      uint32_t used = 0;                                             // phase of each stage's tail barrier, one bit each
+      uint32_t used = 0, at = 0;                                     // used: phase of each stage's tail barrier, one bit each
       bool ok = true;
-      for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next()) {
-        const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
+      for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next(), ++at) {
+        const Tile T = read_tile(at, ok);
+        if (!ok) break;
         if (T.kb1 == T.kb0) continue;
         stage = (stage + T.kb1 - T.kb0 - 1) % C::kStages;            // this unit's last block
         const int rem = T.len - (T.kb1 - 1) * kBK;
@@ -421,9 +453,9 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
           // a K row is one 128-byte line of each box (the swizzle stays inside
           // the line): the rows to clear are one piece per box
           const int bytes = (((rem + 15) & ~15) - rem) * 128, boxes = (((T.n + 15) & ~15) / 2 + 63) >> 6;
-          const uint32_t at = stage * C::A_BYTES + rem * 128 + lane * 16;
+          const uint32_t first = stage * C::A_BYTES + rem * 128 + lane * 16;
           for (int i = lane * 16; i < bytes; i += 512) {
-            const uint32_t o = sbase + at + (i - lane * 16);
+            const uint32_t o = sbase + first + (i - lane * 16);
             sts128(o + C::OFF_A, make_uint4(0, 0, 0, 0));
             sts128(o + C::OFF_A + 8192, make_uint4(0, 0, 0, 0));
             sts128(o + C::OFF_B, make_uint4(0, 0, 0, 0));
@@ -448,8 +480,14 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     uint8_t* sbuf = smem + C::OFF_EPI + (warp - 4) * C::EPI_WARP_BYTES;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (Walk<kMode> w(unit, units); w.tile() < ntiles; w.next()) {
-      const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
+    uint32_t at = 0;
+    for (Walk<kMode> w(unit, units); w.tile() < ntiles; w.next(), ++at) {
+      bool ok;
+      const Tile T = read_tile(at, ok);
+      if (!ok) {
+        if (lane == 0) raise_device_error(kErrTimeout);
+        break;
+      }
       const int row = T.r0 + rank * 128 + q * 32;                // this warp's 32 M-side rows
       const int chunks = (T.n + 31) >> 5;
       const bool any = T.kb1 != T.kb0;                           // kWgrad: an expert without rows has a zero gradient
