@@ -499,18 +499,14 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         }
         tc_fence_after();
       }
-      for (int c = h; c < chunks; c += 2) {
-        uint32_t r[32];
-        if (any) {
-          tmem_ld_32x32b_x32(tmem_base + (uint32_t(q * 32) << 16) + acc * C::BN + 32 * c, r);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0u;
-        }
-        if (p.splits > 1) {
-          // fp32 sums as they lie: kWgrad 32 columns of a row per lane, else a
-          // column per lane
+      const uint32_t from = tmem_base + (uint32_t(q * 32) << 16) + acc * C::BN;
+      uint32_t r[32];
+      if (p.splits > 1) {
+        // fp32 sums as they lie: kWgrad 32 columns of a row per lane, else a
+        // column per lane
+        for (int c = h; c < chunks; c += 2) {
+          tmem_ld_32x32b_x32(from + 32 * c, r);
+          tmem_wait_ld(r);
           if (row + lane < p.rows) {
             if constexpr (kMode == kWgrad) {
               float* dst = p.sums + ((int64_t(T.part) * p.E + T.e) * p.rows + row + lane) * p.cols + T.c0 + 32 * c;
@@ -525,66 +521,77 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                 if (32 * c + j < T.n) dst[int64_t(j) * p.rows] = __uint_as_float(r[j]);
             }
           }
-          continue;
         }
-        if constexpr (kMode == kWgrad) {
-          // one row of 32 columns per lane: staged in the store map's 64-byte
-          // swizzle (16-byte piece j of row r at j ^ ((r >> 1) & 3)); the map
-          // clips the box at the matrix's edges
-          if (row < p.rows) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack16x2<kDt>(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1]));
-              *reinterpret_cast<uint4*>(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tmap_o, smem_u32(sbuf), T.c0 + 32 * c, row, T.e);
-              bulk_commit();
-            }
+      } else {
+        // kWgrad: 32 columns of a row per lane; else fragments for a transposed
+        // store, lanes 0..15 and 16..31
+        auto load = [&](int c) {
+          if constexpr (kMode == kWgrad) {
+            tmem_ld_32x32b_x32(from + 32 * c, r);
+          } else {
+            tmem_ld_16x256b_x4(from + 32 * c, r);
+            tmem_ld_16x256b_x4(from + 32 * c + (16u << 16), r + 16);
           }
-        } else {
-          // lane = output column, register = token: transposed through shared
-          // memory (a token's 32 columns are one 64-byte line, written two
-          // bytes a lane without conflicts).  A chunk of 32 tokens leaves by
-          // TMA (64-byte swizzle: piece j of line t at j ^ ((t >> 1) & 3); the
-          // map clips the columns), the segment's last tokens by 16-byte stores
-          // of four lanes a token
-          const bool whole = 32 * c + 32 <= T.n;
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
+        };
+        if (any && h < chunks) load(h);
+        for (int c = h; c < chunks; c += 2) {
+          uint32_t w[16];
+          if (any) {
+            tmem_wait_ld(r);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t w = pack16x2<kDt>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            uint8_t* line = sbuf + (2 * j) * 64 + (((lane >> 3) ^ (j & 3)) << 4) + (lane & 7) * 2;
-            *reinterpret_cast<uint16_t*>(line) = uint16_t(w & 0xFFFFu);
-            *reinterpret_cast<uint16_t*>(line + 64) = uint16_t(w >> 16);
+            for (int j = 0; j < 16; ++j) w[j] = pack16x2<kDt>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            if (c + 2 < chunks) load(c + 2);                       // on its way while this chunk is stored
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = 0u;
           }
-          if (whole) {
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && row < p.rows) {
-              tma_store_2d(&tmap_o, smem_u32(sbuf), row, T.t0 + 32 * c);
-              bulk_commit();
+          if constexpr (kMode == kWgrad) {
+            // staged in the store map's 64-byte swizzle (16-byte piece j of row
+            // r at j ^ ((r >> 1) & 3)); the map clips the box at the matrix's edges
+            if (row < p.rows) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&tmap_o, smem_u32(sbuf), T.c0 + 32 * c, row, T.e);
+                bulk_commit();
+              }
             }
           } else {
+            // w[2 g + (0, 1)]: tokens 8 g.. of lanes 0..7 and 8..15; w[8 + ..] of
+            // lanes 16..31.  A token's 32 columns become one 64-byte line (piece j
+            // of line t at j ^ ((t >> 1) & 3)).  A chunk of 32 tokens leaves by
+            // TMA (the map clips the columns), the segment's last tokens by
+            // 16-byte stores of four lanes a token
+            if (lane == 0) bulk_wait_read_all();
             __syncwarp();
-            const int col = row + (lane & 3) * 8;
+            const uint32_t to = smem_u32(sbuf) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = 8 * i + (lane >> 2);
-              const uint4 v = *reinterpret_cast<const uint4*>(sbuf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
-              if (32 * c + tok < T.n && col < p.rows)
-                *reinterpret_cast<uint4*>(p.out + int64_t(T.t0 + 32 * c + tok) * p.rows + col) = v;
+            for (int g = 0; g < 4; ++g) stmatrix_x4_trans(to + g * 512, w[2 * g], w[2 * g + 1], w[8 + 2 * g], w[9 + 2 * g]);
+            if (32 * c + 32 <= T.n) {
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0 && row < p.rows) {
+                tma_store_2d(&tmap_o, smem_u32(sbuf), row, T.t0 + 32 * c);
+                bulk_commit();
+              }
+            } else {
+              __syncwarp();
+              const int col = row + (lane & 3) * 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int tok = 8 * i + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4*>(sbuf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
+                if (32 * c + tok < T.n && col < p.rows)
+                  *reinterpret_cast<uint4*>(p.out + int64_t(T.t0 + 32 * c + tok) * p.rows + col) = v;
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }
