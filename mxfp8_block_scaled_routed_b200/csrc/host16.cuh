@@ -253,7 +253,7 @@ int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N,
   MX_TRY(make_map16(&ma, dtype, w, 3, K, N, E, 64, transpose_w ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B, "weights"));
   MX_TRY(make_map16(&mb, dtype, a, 2, p.kext, M, 1, 64, ragged::Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
   mo = mb;   // (fewer than 32 tokens: no chunk of 32 to store)
-  if (M >= 32) MX_TRY(make_map16(&mo, dtype, out, 2, p.rows, M, 1, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "output"));
+  if (M >= 32) MX_TRY(make_map16(&mo, dtype, out, 2, p.rows, M, 1, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, "output"));
   const int64_t tiles = ragged_tiles(M, N, K, E, transpose_w);
   return transpose_w ? launch_ragged<ragged::kDgrad>(dtype, ma, mb, mo, p, tiles, d, stream)
                      : launch_ragged<ragged::kFwd>(dtype, ma, mb, mo, p, tiles, d, stream);

@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int OFF_A = 0, OFF_B = kStages * A_BYTES;
   static_assert(A_BYTES == B_BYTES, "one stage offset for both operands");
   static constexpr int OFF_EPI = OFF_B + kStages * B_BYTES;
-  static constexpr int EPI_WARP_BYTES = 2048;  // one 32 x 32 block of 16-bit outputs per warp
+  static constexpr int EPI_WARP_BYTES = 2048;  // a 32 x 32 block of 16-bit outputs per epilogue warp
   static constexpr int OFF_BAR = OFF_EPI + 8 * EPI_WARP_BYTES;
   static constexpr int kInfo = 16;             // tiles that the producer may announce ahead
   static constexpr int NUM_BARS = 3 * kStages + 4 + 2 * kInfo;
@@ -123,6 +123,18 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
   return ok != 0;
+}
+
+// A barrier of two warps: whether both say yes.
+__device__ __forceinline__ bool pair_all(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.and.pred q, %2, 64, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(uint32_t(yes)), "r"(id)
+      : "memory");
+  return r != 0;
 }
 
 // The tiles of one pair, a round over all pairs at a time; kWgrad's odd rounds
@@ -477,28 +489,30 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   } else if (warp >= 4) {
     // ================= epilogue
     const int q = warp & 3, h = (warp - 4) >> 2;
-    uint8_t* sbuf = smem + C::OFF_EPI + (warp - 4) * C::EPI_WARP_BYTES;
+    constexpr bool kW = kMode == kWgrad;
+    // kFwd / kDgrad: the warps of neighbouring lanes share two buffers, so that a
+    // store box has whole 128-byte lines (64 features of 32 tokens): 36204 rows x
+    // 3784 x 40 111 -> 98 us, 8 experts x 2048 x 512 63 -> 60.  kWgrad keeps a
+    // buffer a warp: its two warps of the same lanes on one box took 429 for 441 us
+    // on tiles of 12 K blocks and 128 for 115 on tiles of two
+    const int pair = (warp - 4) >> 1, side = q & 1;
+    uint8_t* sbuf = smem + C::OFF_EPI + (kW ? (warp - 4) * C::EPI_WARP_BYTES : pair * 2 * C::EPI_WARP_BYTES);
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t at = 0;
     for (Walk<kMode> w(unit, units); w.tile() < ntiles; w.next(), ++at) {
       bool ok;
       const Tile T = read_tile(at, ok);
-      if (!ok) {
-        if (lane == 0) raise_device_error(kErrTimeout);
-        break;
-      }
       const int row = T.r0 + rank * 128 + q * 32;                // this warp's 32 M-side rows
       const int chunks = (T.n + 31) >> 5;
       const bool any = T.kb1 != T.kb0;                           // kWgrad: an expert without rows has a zero gradient
-      if (!any && p.splits > 1) continue;                        // (join_kernel writes it)
-      if (any) {
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase))) {
-          if (lane == 0) raise_device_error(kErrTimeout);
-          break;
-        }
-        tc_fence_after();
+      if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase));
+      if (!(kW ? ok : pair_all(1 + pair, ok))) {                 // (two that share a buffer leave together)
+        if (lane == 0) raise_device_error(kErrTimeout);
+        break;
       }
+      if (!any && p.splits > 1) continue;                        // (join_kernel writes it)
+      tc_fence_after();
       const uint32_t from = tmem_base + (uint32_t(q * 32) << 16) + acc * C::BN;
       uint32_t r[32];
       if (p.splits > 1) {
@@ -564,19 +578,19 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             }
           } else {
             // w[2 g + (0, 1)]: tokens 8 g.. of lanes 0..7 and 8..15; w[8 + ..] of
-            // lanes 16..31.  A token's 32 columns become one 64-byte line (piece j
-            // of line t at j ^ ((t >> 1) & 3)).  A chunk of 32 tokens leaves by
-            // TMA (the map clips the columns), the segment's last tokens by
-            // 16-byte stores of four lanes a token
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-            const uint32_t to = smem_u32(sbuf) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+            // lanes 16..31.  A token's 64 columns become one line (piece j of line
+            // t at j ^ (t & 7)).  A chunk of 32 tokens leaves by TMA (the map
+            // clips the columns), the segment's last tokens by 16-byte stores of
+            // four lanes a token
+            if (side == 0 && lane == 0) bulk_wait_read_all();
+            named_bar_sync(1 + pair, 64);
+            const uint32_t to = smem_u32(sbuf) + (lane & 7) * 128 + (((4 * side + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) stmatrix_x4_trans(to + g * 512, w[2 * g], w[2 * g + 1], w[8 + 2 * g], w[9 + 2 * g]);
+            for (int g = 0; g < 4; ++g) stmatrix_x4_trans(to + g * 1024, w[2 * g], w[2 * g + 1], w[8 + 2 * g], w[9 + 2 * g]);
             if (32 * c + 32 <= T.n) {
               fence_proxy_async();
-              __syncwarp();
-              if (lane == 0 && row < p.rows) {
+              named_bar_sync(1 + pair, 64);
+              if (side == 0 && lane == 0 && row < p.rows) {
                 tma_store_2d(&tmap_o, smem_u32(sbuf), row, T.t0 + 32 * c);
                 bulk_commit();
               }
@@ -586,7 +600,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int tok = 8 * i + (lane >> 2);
-                const uint4 v = *reinterpret_cast<const uint4*>(sbuf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
+                const uint4 v =
+                    *reinterpret_cast<const uint4*>(sbuf + tok * 128 + (((4 * side + (lane & 3)) ^ (tok & 7)) << 4));
                 if (32 * c + tok < T.n && col < p.rows)
                   *reinterpret_cast<uint4*>(p.out + int64_t(T.t0 + 32 * c + tok) * p.rows + col) = v;
               }
