@@ -101,11 +101,11 @@ int make_map16(CUtensorMap* map, int dtype, const void* base, int rank, int64_t 
   return MXMOE_OK;
 }
 
-template <int kMode, int kDt>
+template <int kMode, int kDt, bool kPair>
 int launch_ragged_dt(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const ragged::Params& p,
                      int64_t max_tiles, const DevInfo* d, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto kern = ragged::ragged_gemm_kernel<kMode, kDt>;
+  auto kern = ragged::ragged_gemm_kernel<kMode, kDt, kPair>;
   MX_TRY(ensure_smem(kern, done, ragged::Cfg::SMEM_BYTES));
   max_tiles *= p.splits;
   if (max_tiles > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "%lld tiles: too large", (long long)max_tiles);
@@ -133,11 +133,11 @@ int launch_ragged_dt(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
   return MXMOE_OK;
 }
 
-template <int kMode>
+template <int kMode, bool kPair>
 int launch_ragged(int dtype, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                   const ragged::Params& p, int64_t max_tiles, const DevInfo* d, cudaStream_t stream) {
-  return dtype == MXMOE_BF16 ? launch_ragged_dt<kMode, kBF16>(ma, mb, mo, p, max_tiles, d, stream)
-                             : launch_ragged_dt<kMode, kFP16>(ma, mb, mo, p, max_tiles, d, stream);
+  return dtype == MXMOE_BF16 ? launch_ragged_dt<kMode, kBF16, kPair>(ma, mb, mo, p, max_tiles, d, stream)
+                             : launch_ragged_dt<kMode, kFP16, kPair>(ma, mb, mo, p, max_tiles, d, stream);
 }
 
 int check_ragged(int64_t M, int64_t N, int64_t K, int E, const int32_t* offsets, int dtype) {
@@ -255,8 +255,8 @@ int mxmoe_ragged_gemm(const void* a, int64_t M, const void* w, int E, int64_t N,
   mo = mb;   // (fewer than 32 tokens: no chunk of 32 to store)
   if (M >= 32) MX_TRY(make_map16(&mo, dtype, out, 2, p.rows, M, 1, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, "output"));
   const int64_t tiles = ragged_tiles(M, N, K, E, transpose_w);
-  return transpose_w ? launch_ragged<ragged::kDgrad>(dtype, ma, mb, mo, p, tiles, d, stream)
-                     : launch_ragged<ragged::kFwd>(dtype, ma, mb, mo, p, tiles, d, stream);
+  return transpose_w ? launch_ragged<ragged::kDgrad, true>(dtype, ma, mb, mo, p, tiles, d, stream)
+                     : launch_ragged<ragged::kFwd, true>(dtype, ma, mb, mo, p, tiles, d, stream);
 }
 
 int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, int64_t M,
@@ -283,9 +283,18 @@ int mxmoe_ragged_gemm_wgrad(const void* g, int64_t N, const void* a, int64_t K, 
   CUtensorMap ma, mb, mo;
   MX_TRY(make_map16(&ma, dtype, g, 2, N, M, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "gradients"));
   MX_TRY(make_map16(&mb, dtype, a, 2, K, M, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "tokens"));
-  MX_TRY(make_map16(&mo, dtype, dw, 3, K, N, E, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "weight gradients"));
+  // Boxes of 64 columns leave whole 128-byte lines, but tie two epilogue warps to
+  // each other.  They gain where rows start off the 32-byte sectors (44 experts of 31
+  // rows, 456 x 6776: 79 / 95 us) and where tiles have six K blocks or more on average
+  // (64 x 1408 x 2048: 469 rows an expert 159 / 168, 768 rows x 2816 429 / 447);
+  // shorter tiles wait for the epilogue (312 rows 127 / 125, 94 rows of 2048 x 2048
+  // 127 / 121, one row of 4096 x 2048 209 / 178).
+  const bool pair = K % 16 != 0 || M >= int64_t(400) * E;
+  MX_TRY(make_map16(&mo, dtype, dw, 3, K, N, E, pair ? 64 : 32, 32,
+                    pair ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, "weight gradients"));
   const int64_t tiles = ragged_tiles(M, N, K, E, 2);
-  return launch_ragged<ragged::kWgrad>(dtype, ma, mb, mo, p, tiles, d, stream);
+  return pair ? launch_ragged<ragged::kWgrad, true>(dtype, ma, mb, mo, p, tiles, d, stream)
+              : launch_ragged<ragged::kWgrad, false>(dtype, ma, mb, mo, p, tiles, d, stream);
 }
 
 int mxfp8_swiglu_ckpt(const void* h13, int64_t rows, int64_t F, const int32_t* rows_dev, int dtype, void* h,

@@ -218,7 +218,8 @@ __device__ __forceinline__ Tile get_tile(const Params& p, const int32_t* offs, c
   return T;
 }
 
-template <int kMode, int kDt>
+// kPair: store boxes of 64 values instead of 32 (kFwd and kDgrad: always).
+template <int kMode, int kDt, bool kPair>
 __global__ void __launch_bounds__(384, 1)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                    const __grid_constant__ CUtensorMap tmap_o, const Params p) {
@@ -490,13 +491,17 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     // ================= epilogue
     const int q = warp & 3, h = (warp - 4) >> 2;
     constexpr bool kW = kMode == kWgrad;
-    // kFwd / kDgrad: the warps of neighbouring lanes share two buffers, so that a
-    // store box has whole 128-byte lines (64 features of 32 tokens): 36204 rows x
-    // 3784 x 40 111 -> 98 us, 8 experts x 2048 x 512 63 -> 60.  kWgrad keeps a
-    // buffer a warp: its two warps of the same lanes on one box took 429 for 441 us
-    // on tiles of 12 K blocks and 128 for 115 on tiles of two
-    const int pair = (warp - 4) >> 1, side = q & 1;
-    uint8_t* sbuf = smem + C::OFF_EPI + (kW ? (warp - 4) * C::EPI_WARP_BYTES : pair * 2 * C::EPI_WARP_BYTES);
+    static_assert(kW || kPair, "kFwd and kDgrad store boxes of 64 columns");
+    // Two warps may share a buffer, so that a store box has whole 128-byte lines:
+    // the warps of neighbouring lanes in kFwd / kDgrad (64 features of 32 tokens;
+    // 36204 rows x 3784 x 40 111 -> 98 us, 8 experts x 2048 x 512 63 -> 60), the two
+    // of the same lanes in kWgrad where the host chose that (64 columns of 32 rows)
+    const int pair = kW ? q : (warp - 4) >> 1, side = kPair ? (kW ? h : q & 1) : 0;
+    uint8_t* sbuf = smem + C::OFF_EPI + (kPair ? pair * 2 : warp - 4) * C::EPI_WARP_BYTES;
+    auto sync = [&]() {
+      if constexpr (kPair) named_bar_sync(1 + pair, 64);
+      else __syncwarp();
+    };
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t at = 0;
@@ -507,7 +512,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const int chunks = (T.n + 31) >> 5;
       const bool any = T.kb1 != T.kb0;                           // kWgrad: an expert without rows has a zero gradient
       if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase));
-      if (!(kW ? ok : pair_all(1 + pair, ok))) {                 // (two that share a buffer leave together)
+      if (!(kPair ? pair_all(1 + pair, ok) : ok)) {             // (two that share a buffer leave together)
         if (lane == 0) raise_device_error(kErrTimeout);
         break;
       }
@@ -547,31 +552,37 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             tmem_ld_16x256b_x4(from + 32 * c + (16u << 16), r + 16);
           }
         };
-        if (any && h < chunks) load(h);
-        for (int c = h; c < chunks; c += 2) {
+        // (kWgrad: where an odd number of chunks leaves the second of two warps that
+        // share a buffer without a last one, it stages what it finds: that half of
+        // the box lies past the matrix)
+        const int last = kW && kPair ? (chunks + 1) & ~1 : chunks;
+        if (any && h < last) load(h);
+        for (int c = h; c < last; c += 2) {
           uint32_t w[16];
           if (any) {
             tmem_wait_ld(r);
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack16x2<kDt>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            if (c + 2 < chunks) load(c + 2);                       // on its way while this chunk is stored
+            if (c + 2 < last) load(c + 2);                         // on its way while this chunk is stored
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = 0u;
           }
           if constexpr (kMode == kWgrad) {
-            // staged in the store map's 64-byte swizzle (16-byte piece j of row
-            // r at j ^ ((r >> 1) & 3)); the map clips the box at the matrix's edges
+            // staged in the store map's swizzle: 16-byte piece j of row r at j ^
+            // (r & 7) of 128-byte lines, at j ^ ((r >> 1) & 3) of 64-byte ones; the
+            // map clips the box at the matrix's edges
             if (row < p.rows) {
-              if (lane == 0) bulk_wait_read_all();
-              __syncwarp();
+              if (side == 0 && lane == 0) bulk_wait_read_all();
+              sync();
+              const int line = lane * (kPair ? 128 : 64), turn = kPair ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                *reinterpret_cast<uint4*>(sbuf + line + (((4 * side + j) ^ turn) << 4)) =
                     make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
               fence_proxy_async();
-              __syncwarp();
-              if (lane == 0) {
+              sync();
+              if (side == 0 && lane == 0) {
                 tma_store_3d(&tmap_o, smem_u32(sbuf), T.c0 + 32 * c, row, T.e);
                 bulk_commit();
               }
@@ -583,13 +594,13 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             // clips the columns), the segment's last tokens by 16-byte stores of
             // four lanes a token
             if (side == 0 && lane == 0) bulk_wait_read_all();
-            named_bar_sync(1 + pair, 64);
+            sync();
             const uint32_t to = smem_u32(sbuf) + (lane & 7) * 128 + (((4 * side + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll
             for (int g = 0; g < 4; ++g) stmatrix_x4_trans(to + g * 1024, w[2 * g], w[2 * g + 1], w[8 + 2 * g], w[9 + 2 * g]);
             if (32 * c + 32 <= T.n) {
               fence_proxy_async();
-              named_bar_sync(1 + pair, 64);
+              sync();
               if (side == 0 && lane == 0 && row < p.rows) {
                 tma_store_2d(&tmap_o, smem_u32(sbuf), row, T.t0 + 32 * c);
                 bulk_commit();

@@ -67,6 +67,22 @@ def test_weight_gradient_of_whole_numbers_is_exact(lens, N, K, dt):
     assert mxk.device_error() == 0
 
 
+@pytest.mark.parametrize("lens", [[3, 0, 40], [500, 410], [0, 2000]], ids=["short", "long", "one"])
+@pytest.mark.parametrize("N,K", [(136, 272), (264, 288), (24, 16), (520, 600), (8, 344), (40, 200)])
+def test_weight_gradient_edges_of_store_boxes(lens, N, K):
+    """Boxes of 32 and of 64 columns (few or many rows an expert, row pitch), odd numbers of 32-column pieces,
+    bytes behind the matrix untouched."""
+    g = np.random.default_rng(21)
+    off = P.offsets_of(lens)
+    R, E = sum(lens), len(lens)
+    gr, a = _ints(g, R, N), _ints(g, R, K)
+    flat = torch.full((E * N * K + 64,), 5.0, dtype=BF, device=DEV)
+    out = flat[: E * N * K].view(E, N, K)
+    mxk.mxmoe_ragged_gemm_wgrad(gr.to(DEV, BF), a.to(DEV, BF), off.to(DEV), out=out)
+    P.assert_same(out, _round(P.wgrad(gr, a, off)[0], BF), "dw")
+    assert (flat[E * N * K :] == 5.0).all() and mxk.device_error() == 0
+
+
 @pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
 def test_normal_values_within_the_bound(dt):
     g = torch.Generator().manual_seed(3)
