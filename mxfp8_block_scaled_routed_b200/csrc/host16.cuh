@@ -225,7 +225,7 @@ size_t carve_decode(uint8_t* base, int64_t S, int64_t D, int64_t F, DecodeWs* w)
 extern "C" {
 
 size_t mxmoe_ragged_workspace_size(int64_t M, int64_t N, int64_t K, int E, int which) {
-  if (M <= 0 || N <= 0 || K <= 0 || E <= 0 || which < 0 || which > 2 || N >= (int64_t(1) << 30) || K >= (int64_t(1) << 30) ||
+  if (M <= 0 || N <= 0 || K <= 0 || E <= 0 || E > ragged::kMaxE || which < 0 || which > 2 || N >= (int64_t(1) << 30) || K >= (int64_t(1) << 30) ||
       M > (int64_t(1) << 31))
     return 0;
   const int splits = ragged_splits(ragged_tiles(M, N, K, E, which), ragged_blocks(M, N, K, which));

@@ -26,11 +26,18 @@
 // loads for 512 cycles of MMA where a single CTA's 128 x 256 tile would need
 // 48 KB.
 //
-// CTA = 12 warps: warp 0 issues TMA, warp 1 of the even CTA issues the pair's
-// MMAs, warp 2 owns TMEM, warp 3 clears kWgrad tails, warps 4..11 are the
-// epilogue (warp 4 + q and 8 + q read TMEM lanes 32 q.., alternating 32-column
-// chunks).  Two accumulators of 256 columns: a tile's epilogue runs beside the
-// next tile's MMAs.
+// CTA = 12 warps: warp 0 works out each tile's place and issues TMA, warp 1 of
+// the even CTA issues the pair's MMAs, warp 2 owns TMEM, warp 3 clears kWgrad
+// tails, warps 4..11 are the epilogue (warp 4 + q and 8 + q read TMEM lanes
+// 32 q.., alternating 32-column chunks).  Two accumulators of 256 columns: a
+// tile's epilogue runs beside the next tile's MMAs.
+//
+// Bound by the MMAs (512 cycles a full K block) from about ten K blocks a tile
+// on, and in a loop by the power limit (49152 rows, 64 x 2816 x 2048: 440 us,
+// 1.29 PFLOP/s); below that by the epilogue's ~4,500 cycles a tile, a chain of
+// TMEM read, staging, proxy fence and store per chunk (32768 rows, 8 x 4096 x
+// 256: 74 us, 3.6 TB/s of stores).  Few tiles with a long contraction are split
+// along it and joined (join_kernel).
 #pragma once
 #include <cuda.h>
 #include "half16.cuh"

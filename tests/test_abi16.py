@@ -54,6 +54,14 @@ def test_ragged_workspace_arithmetic(L):
     assert f(0, 16, 24, 1, 0) == 0 and f(10, 16, 24, 0, 0) == 0 and f(10, 16, 24, 1, 3) == 0
 
 
+def test_ragged_workspace_of_refused_sizes_is_zero(L):
+    f = L.mxmoe_ragged_workspace_size
+    assert f(4096, 24, 72, 1024, 2) >= 0
+    for M, N, K, E, which in ((4096, 24, 72, 1025, 2), ((1 << 31) + 1, 24, 72, 1, 2), (4096, 1 << 30, 72, 1, 2), (4096, 24, 1 << 30, 1, 2),
+                              (4096, (1 << 30) - 8, (1 << 30) - 8, (1 << 31) - 1, 2), (4096, 24, 72, 1, 3), (4096, 24, 72, 0, 2), (-1, 24, 72, 1, 2)):
+        assert f(M, N, K, E, which) == 0, (M, N, K, E, which)
+
+
 def test_ragged_wgrad_refusals(L):
     ok = dict(g=FAKE, N=16, a=FAKE, K=24, M=10, off=FAKE, E=2, dt=1, out=FAKE)
 
