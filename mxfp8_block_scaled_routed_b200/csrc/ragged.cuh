@@ -34,7 +34,7 @@
 //
 // Bound by the MMAs (512 cycles a full K block) from about ten K blocks a tile
 // on, and in a loop by the power limit (49152 rows, 64 x 2816 x 2048: 440 us,
-// 1.29 PFLOP/s); below that by the epilogue's ~4,500 cycles a tile, a chain of
+// 1.29 PFLOP/s); below that by the epilogue's ~4,100 cycles a tile, a chain of
 // TMEM read, staging, proxy fence and store per chunk (32768 rows, 8 x 4096 x
 // 256: 74 us, 3.6 TB/s of stores).  Few tiles with a long contraction are split
 // along it and joined (join_kernel).
