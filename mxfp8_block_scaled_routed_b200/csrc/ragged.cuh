@@ -34,10 +34,11 @@
 //
 // Bound by the MMAs (512 cycles a full K block) from about ten K blocks a tile
 // on, and in a loop by the power limit (49152 rows, 64 x 2816 x 2048: 440 us,
-// 1.29 PFLOP/s); below that by the epilogue's ~4,100 cycles a tile, a chain of
-// TMEM read, staging, proxy fence and store per chunk (32768 rows, 8 x 4096 x
-// 256: 74 us, 3.6 TB/s of stores).  Few tiles with a long contraction are split
-// along it and joined (join_kernel).
+// 1.29 PFLOP/s).  Shorter tiles wait for their stores: a chunk's staging buffer
+// is free 300 to 490 cycles late while the tiles' loads and stores together move
+// 11 TB/s through L2 (32768 rows, 8 x 4096 x 256: 73 us, ~3,700 cycles a tile of
+// 2,048 of MMAs; long contractions load 13 TB/s).  Few tiles with a long
+// contraction are split along it and joined (join_kernel).
 #pragma once
 #include <cuda.h>
 #include "half16.cuh"
