@@ -482,14 +482,16 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
             sts128(o + C::OFF_B, make_uint4(0, 0, 0, 0));
             if (boxes > 1) sts128(o + C::OFF_B + 8192, make_uint4(0, 0, 0, 0));
           }
-          // the rows lie in this CTA's own shared memory, and its own tensor core
-          // reads them: the proxy fence is what orders the two, the arrival only
-          // tells the issuer.  (fence.proxy.async over all state spaces and a
-          // cluster-scope release took ~1,900 cycles a tile more, 464 against 416 us
-          // on 64 experts of 760 rows.)
+          // the issuer of the MMAs that read these rows is a thread of the even
+          // CTA: every lane's stores are fenced to the async proxy, the warp sync
+          // orders them before lane 0's release, and that one has to be of cluster
+          // scope to pair with the issuer's acquire.  Only shared memory is
+          // published: a release of all state spaces waits for the stores under way
+          // (64 experts of 760 rows x 2816 x 2048 463 us against 423, 64 of 94 rows
+          // x 2048 x 2048 146 against 136)
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(full_bar(stage), 0);
+          if (lane == 0) mbar_arrive_release_shared(full_bar(stage), 0);
         }
         stage = (stage + 1) % C::kStages;
       }

@@ -61,7 +61,6 @@ __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();  // the .aligned barrier wants every warp converged
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the mbarrier at the same shared-memory offset in CTA `cta` of the cluster.
 // Arrive on the mbarrier at this offset in CTA `cta` of the cluster, with the
 // instruction's default semantics (release at CTA scope).  The accumulator
 // hand-off uses it after tcgen05.wait::ld, when this warp's TMEM reads are
@@ -71,6 +70,18 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, uint32_t cta) {
   asm volatile(
       "{ .reg .b32 ra; mapa.shared::cluster.u32 ra, %0, %1;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [ra]; }" ::"r"(bar),
+      "r"(cta)
+      : "memory");
+}
+// The same with a release at cluster scope of shared-memory accesses only: what
+// this thread wrote to its CTA's shared memory, or saw there by a barrier of its
+// warp or CTA, is there for a thread of the other CTA that acquires at cluster
+// scope.  (A release of all state spaces also waits for global traffic.)
+__device__ __forceinline__ void mbar_arrive_release_shared(uint32_t bar, uint32_t cta) {
+  asm volatile(
+      "{ .reg .b32 ra; mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra]; }" ::"r"(bar),
       "r"(cta)
       : "memory");
 }

@@ -1,0 +1,67 @@
+"""GPU tests of the ragged products where every pair of SMs works through many tiles.
+
+Whole numbers, so results equal the once-rounded exact ones bit for bit; the reference is a float64 product per expert.
+Sizes give each of the 74 pairs more than 16 tiles of several K blocks: stages, accumulators, staging buffers and the
+announced places are all reused, and the parities of their barriers flip several times.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_block_scaled_routed_b200 as mxk
+import plain16 as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, FP = torch.bfloat16, torch.float16
+PAIRS = 74
+
+
+def _ints(g, *shape, top=2):
+    return torch.randint(-top, top + 1, shape, generator=g, device=DEV).double()
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _lens(seed, E, mean):
+    """Odd lengths around the mean (never a multiple of 16), a few experts without rows."""
+    r = np.random.default_rng(seed)
+    n = r.integers(mean // 2, mean + mean // 2 + 1, size=E) | 1
+    n[r.integers(0, E, size=3)] = 0
+    return n.tolist()
+
+
+def _same(got, ref, what):
+    bad = got != ref
+    assert not bad.any(), f"{what}: {int(bad.sum())} values differ, first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("E,mean,N,K", [(48, 60, 1304, 1296), (48, 60, 1304, 1288), (40, 450, 1304, 1296), (24, 150, 2056, 1800)])
+def test_weight_gradients_next_to_nan(E, mean, N, K, dt):
+    """Every other expert's rows are NaN: the rows behind each clean segment's end, up to the next multiple of 16, must have
+    been cleared in both SMs of a pair before the products read them."""
+    g, lens = _gen(1), _lens(1, E, mean)
+    off = P.offsets_of(lens)
+    M = sum(lens)
+    assert E * -(-N // 256) * -(-K // 256) > 16 * PAIRS
+    a, gr = _ints(g, M, K), _ints(g, M, N)
+    pa, pg = a.clone(), gr.clone()
+    for e in range(1, E, 2):
+        pa[off[e]:off[e + 1]], pg[off[e]:off[e + 1]] = float("nan"), float("nan")
+    pa, pg, o = pa.to(dt), pg.to(dt), off.to(DEV)
+    out = torch.full((E, N, K), 7.0, dtype=dt, device=DEV)
+    for _ in range(3):
+        out.fill_(7.0)
+        mxk.mxmoe_ragged_gemm_wgrad(pg, pa, o, out=out)
+        for e in range(E):
+            s = slice(int(off[e]), int(off[e + 1]))
+            if e % 2 and lens[e]:
+                assert torch.isnan(out[e]).all(), e
+            else:
+                _same(out[e], (gr[s].t() @ a[s]).to(dt), f"expert {e} of {lens[e]} rows")
+    assert mxk.device_error() == 0
