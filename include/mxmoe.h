@@ -607,8 +607,11 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *  expert_ids DEVICE int32 [S] in [0, E) (any order, repeats allowed; an id
  *  outside raises MXMOE_ERR_ARG on the device and its row of y is not
  *  written).  Each expert's weights are read once per eight slots it has (fewer
- *  for K above 7168, as shared memory allows).  Products with f16 copies of x (a power of two per row keeps 16-bit inputs
- *  exact down to 2^-36 of the row's largest value), fp32 sums, one rounding.
+ *  for K above 7168, as shared memory allows).  Products with f16 copies of x
+ *  (a power of two per row keeps every bit of an input that weighs 2^-36 of the
+ *  row's largest value or more; an element is off by at most 2^-37 of it), fp32
+ *  sums, one rounding.  Rows and scales of any size: a sum overflows only where
+ *  one of the values themselves would in fp32.
  *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048, S * N / 16 < 2^31, and
  *  shared memory for one f16 row (K up to about 60000).
  * ------------------------------------------------------------------------- */

@@ -478,11 +478,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       }
       return m;
     };
-    // power of two that takes the largest magnitude to [2^12, 2^13): exponent field of its inverse
-    auto inv_exp = [&](int r) {
-      const int ef = int(xmax[r] >> 23);
-      return ef == 0 ? 127 : min(254, max(1, 127 + 12 - (ef - 127)));
-    };
+    // power of two that takes the largest magnitude to [2^12, 2^13), 2^127 at most
+    // (rows below 2^-114: what f16 holds then goes down to 2^-151, beyond the inputs'
+    // own last bits): its exponent field, 12 .. 254
+    auto inv_exp = [&](int r) { return min(254, 127 + 12 + 127 - int(xmax[r] >> 23)); };
     auto put = [&](int r, int c, const float (&f)[8]) {
       const float inv = __uint_as_float(uint32_t(inv_exp(r)) << 23);
       uint8_t* at = xs + ((int64_t(c >> 2) * p.group + r) * 4 + (c & 3)) * 16;
@@ -546,12 +545,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         }
       }
     }
-    float xscale[2];                                           // 2^exponent of columns 2q, 2q + 1
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 2 * q + i;
-      xscale[i] = r < n ? e8m0_to_f32(uint32_t(254 - inv_exp(r))) : 0.0f;
-    }
+    // its inverse as two factors, of exponents -124 .. 100 and -3 .. 15
+    auto down1 = [&](int r) { return max(-124, min(100, 127 - inv_exp(r))); };
+    auto pow2 = [](int e) { return __uint_as_float(uint32_t(127 + e) << 23); };
+    const float xs1[2] = {pow2(down1(2 * q)), pow2(down1(2 * q + 1))};         // (of no slot: its sums are zero)
     __syncthreads();
     // this lane's column of a 32-block; columns past the group's slots read one zero piece
     const uint32_t xlane = g < n ? sm100::smem_u32(xs) + (g * 4 + q) * 16 : sm100::smem_u32(&zero);
@@ -560,6 +557,35 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     for (int tile = tile0 + team; tile < tile1; tile += teams) {
       // ---- this warp's cells of the tile
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto multiply = [&](uint4 wa, uint4 wb, uint32_t sa, uint32_t sb, uint32_t xat, bool down) {   // a cell's products
+        float fa[4], fb[4];
+        e8m0x4_to_f32(sa, fa);
+        e8m0x4_to_f32(sb, fb);
+        const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 xv = lds128(xat + j * xstep);
+          uint32_t ha[4], hb[4];
+          e2m1x8_to_f16(a[j], ha);
+          e2m1x8_to_f16(b[j], hb);
+          float d[4];
+          mma_f16_16816_zero(d, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
+          mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
+          if constexpr (kPieces == 2) {
+            const uint4 xl = lds128(xat + j * xstep + xplane);
+            mma_f16_16816(d, ha[0], hb[0], ha[1], hb[1], xl.x, xl.y);
+            mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xl.z, xl.w);
+          }
+          if (down) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] *= xs1[k & 1];
+          }
+          acc[0] = fmaf(d[0], fa[j], acc[0]);
+          acc[1] = fmaf(d[1], fa[j], acc[1]);
+          acc[2] = fmaf(d[2], fb[j], acc[2]);
+          acc[3] = fmaf(d[3], fb[j], acc[3]);
+        }
+      };
       for (int i = 0; i < mine; i += kMvCells) {
         // the oldest load has come: into registers, and its slot takes the
         // next one before the products (a missing second cell: stale bytes,
@@ -583,29 +609,28 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
 #pragma unroll
         for (int c = 0; c < kMvCells; ++c) {
           if (c > 0 && i + c >= mine) break;
-          float fa[4], fb[4];
-          e8m0x4_to_f32(sa[c], fa);
-          e8m0x4_to_f32(sb[c], fb);
-          const uint32_t a[4] = {wa[c].x, wa[c].y, wa[c].z, wa[c].w}, b[4] = {wb[c].x, wb[c].y, wb[c].z, wb[c].w};
+          multiply(wa[c], wb[c], sa[c], sb[c], xb + 4 * c * xstep, false);
+        }
+      }
+      // ---- the sums lose the row's power of two.  Lifted by it they may have
+      // overflowed where the result does not (scales far above 1): then the tile is
+      // taken again, each block's sum brought down before its scale meets it.  (A
+      // block's sum is a multiple of 2^-25 below 2^21, which the first factor neither
+      // rounds nor overflows.  On eight tokens 199.6 us, without the second look 197;
+      // every block that way 213; chosen by the scales on the way 205.)
+      const bool finite = isfinite(acc[0]) && isfinite(acc[1]) && isfinite(acc[2]) && isfinite(acc[3]);
+      if (__all_sync(0xffffffffu, finite)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 xv = lds128(xb + (4 * c + j) * xstep);
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_f16(a[j], ha);
-            e2m1x8_to_f16(b[j], hb);
-            float d[4];
-            mma_f16_16816_zero(d, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
-            mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
-            if constexpr (kPieces == 2) {
-              const uint4 xl = lds128(xb + (4 * c + j) * xstep + xplane);
-              mma_f16_16816(d, ha[0], hb[0], ha[1], hb[1], xl.x, xl.y);
-              mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xl.z, xl.w);
-            }
-            acc[0] = fmaf(d[0], fa[j], acc[0]);
-            acc[1] = fmaf(d[1], fa[j], acc[1]);
-            acc[2] = fmaf(d[2], fb[j], acc[2]);
-            acc[3] = fmaf(d[3], fb[j], acc[3]);
-          }
+        for (int k = 0; k < 4; ++k) acc[k] *= xs1[k & 1];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
+        const int64_t cell = (int64_t(gexp[grp]) * p.tiles + tile) * cells + cell0;
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+          const uint4* wp = reinterpret_cast<const uint4*>(p.codes + (cell + i) * 1024) + lane;
+          const uint32_t* sp = reinterpret_cast<const uint32_t*>(p.scales + (cell + i) * 64) + g;
+          multiply(__ldg(wp), __ldg(wp + 32), __ldg(sp), __ldg(sp + 8), xlane + (cell0 + i) * 4 * xstep, true);
         }
       }
       // ---- one warp of the team adds the partial sums in warp order and
@@ -628,7 +653,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         const int r = 2 * q + i;
         if (r >= n) continue;
         const int64_t s = order[o0 + r];
-        const float lo = (i ? t.y : t.x) * xscale[i], hi = (i ? t.w : t.z) * xscale[i];
+        const float xs2 = pow2(127 - inv_exp(r) - down1(r)), lo = (i ? t.y : t.x) * xs2, hi = (i ? t.w : t.z) * xs2;
         if constexpr (kGated) {
           static_cast<float*>(p.out)[s * p.tiles * 8 + tile * 8 + g] = silu_mul(lo, hi);
         } else if constexpr (kOut == kF32) {
