@@ -628,8 +628,10 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
  *  x_tokens, out_tokens [T, D] 16-bit; topk_ids int32 and topk_weights fp32
  *  [T, top_k] on the device; an id outside [0, E) raises MXMOE_ERR_ARG there and
  *  adds nothing.  gate, up, h, the experts' outputs and the weighted sum are
- *  held in fp32 (h enters its product as f16, for fp16 layers as two f16 pieces,
- *  scaled by a power of two per slot); one rounding at the end.
+ *  held in fp32 (h enters its product as two f16 pieces, 22 bits, scaled by a power
+ *  of two per slot; where shared memory does not hold two of a row, F above 36224
+ *  with one slot, bf16 layers take one piece and fp16 layers are refused); one
+ *  rounding at the end.
  *  Needs D and F multiples of 128, T * top_k <= 2048, top_k <= E <= 1024.
  *  Workspace: mxfp4_decode_workspace_size() bytes, not shared by calls that
  *  may overlap on the GPU.

@@ -20,6 +20,7 @@
 //             its half 0 and up rows F + 8t.. as its half 1, so that a lane
 //             holds the gate and the up value of the same f.
 #pragma once
+#include <type_traits>
 #include "half16.cuh"
 #include "quant.cuh"
 #include "sm100.cuh"
@@ -183,9 +184,11 @@ fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restr
 // puts the row's largest magnitude at 2^12: bf16 and fp16 inputs keep every
 // bit down to 2^-36 of the row's largest value (an absolute error of at most
 // 2^-37 of it beyond).  The fp32 h between the two products of a layer becomes
-// one f16 (11 bits) where the result is bf16, of whose rounding that is an
-// eighth; where it is fp16, whose error it would raise by 1.4, h goes in as
-// two f16 pieces (22 bits) and takes twice the MMAs.
+// two f16 pieces (22 bits).  Up to four slots have eight columns to themselves:
+// the second pieces are columns 4..7 of the same MMAs, and the two sums meet at
+// the tile's end; more slots take twice the MMAs.  Against one piece (11 bits):
+// one token of 64 x 2048 x 1408 18.0 us for 17.3, eight of 64 x 7168 x 2048 199.9
+// for 195.1, 32 of those (half of the experts with five slots or more) 322 for 292.
 //
 // Bound by HBM: (1/2 + 1/32) N K bytes per expert that has a slot.  A block of
 // 16 warps per SM walks a contiguous range of (slot group, row tile) units;
@@ -194,7 +197,7 @@ fp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restr
 // loads of later tiles are in flight while this one is multiplied, and the
 // warps' partial sums meet in shared memory in a fixed order.
 // Measured on 46 of 64 experts of 7168 x 2048 (1.08 GB of weights, both
-// products and the combine): 198 us, 5.4 TB/s of weights; the loop without its
+// products and the combine): 200 us, 5.4 TB/s of weights; the loop without its
 // products 175 us.  What is left is issue (115 instructions a cell, of which 32
 // conversions, 8 MMAs, 16 FMAs).  12 warps with a ring of three 205 us; bulk
 // copies instead of cp.async 8 % more (about 75 cycles of the issuing warp a
@@ -215,14 +218,15 @@ struct MvArgs {
   int K;
   int team_log2;            // warps that share a tile's cells: 1, 2 or 4 as a power of two (no divisions in a
                             // block's first instructions, which come from L2)
-  int group;                // slots per group, 1..8 (shared memory holds group * K f16)
+  int group;                // slots per group, 1..8 (shared memory holds group * K f16, of fp32 rows `pieces` times)
+  int pieces;               // fp32 rows: f16 pieces of a value; else 1
   const uint8_t* codes;
   const uint8_t* scales;
   void* out;                // gated: fp32 h [S, 8 * tiles]; else y [S, 16 * tiles]
 };
 
-// Types of the activations: kBF16, kFP16, fp32 as one f16 piece, fp32 as two.
-constexpr int kF32 = 2, kF32Two = 3;
+// Types of the activations and of the result: kBF16, kFP16, and fp32.
+constexpr int kF32 = 2;
 
 __host__ __device__ constexpr int mv_smem(int64_t K, int group, int E, int S, int pieces) {
   // ring, partial sums (two tiles), f16 activations, then counts, slot order, groups
@@ -240,7 +244,7 @@ __device__ __forceinline__ void cp_async_wait() {
 
 template <int kDt>
 __device__ __forceinline__ void mv_load8(const void* x, int64_t i, float (&f)[8]) {
-  if constexpr (kDt >= kF32) {
+  if constexpr (kDt == kF32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
     const float4 a = p[0], b = p[1];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -278,9 +282,9 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   uint8_t* ring = mv_smem_raw;                                                    // [warp][slot]: codes, then scales
   float4* red = reinterpret_cast<float4*>(ring + kMvWarps * kMvRing * kMvSlot);   // [2][warp][lane]
   uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * kMvWarps * 32);              // f16 [K/32][group][4 quarters][8]
-  constexpr int kPieces = kDt == kF32Two ? 2 : 1;
   const int plane = p.group * p.K * 2;                                            // bytes of one f16 piece of the group
-  uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + kPieces * plane);              // [8] largest magnitude, fp32 bits
+  const bool two = kDt == kF32 && p.pieces == 2;
+  uint32_t* xmax = reinterpret_cast<uint32_t*>(xs + (two ? 2 * plane : plane));   // [8] largest magnitude, fp32 bits
   int* order = reinterpret_cast<int*>(xmax + 16);                                 // [S] slots, group after group
   int* gexp = order + p.S;                                                        // [S] expert of each group
   int* gstart = gexp + p.S;                                                       // [S + 1] its first place in `order`
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = pack16x2<kFP16>(f[2 * j] * inv, f[2 * j + 1] * inv);
       *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
-      if constexpr (kPieces == 2) {
+      if (two) {
         // what the first piece left (of an infinity: nothing)
         uint32_t l[4];
 #pragma unroll
@@ -548,16 +552,20 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     // its inverse as two factors, of exponents -124 .. 100 and -3 .. 15
     auto down1 = [&](int r) { return max(-124, min(100, 127 - inv_exp(r))); };
     auto pow2 = [](int e) { return __uint_as_float(uint32_t(127 + e) << 23); };
-    const float xs1[2] = {pow2(down1(2 * q)), pow2(down1(2 * q + 1))};         // (of no slot: its sums are zero)
+    // second pieces: in columns 4..7 (packed), or by MMAs of their own
+    const bool packed = two && n <= 4, more = two && n > 4;
+    const int cols = packed ? 3 : 7;                                           // column & cols: slot of a column
+    const float xs1[2] = {pow2(down1(2 * q & cols)), pow2(down1((2 * q + 1) & cols))};   // (of no slot: its sums are zero)
     __syncthreads();
     // this lane's column of a 32-block; columns past the group's slots read one zero piece
-    const uint32_t xlane = g < n ? sm100::smem_u32(xs) + (g * 4 + q) * 16 : sm100::smem_u32(&zero);
-    const int xstep = g < n ? p.group * 64 : 0, xplane = g < n ? plane : 0;
+    const bool live = (g & cols) < n;
+    const uint32_t xlane = live ? sm100::smem_u32(xs) + ((g & cols) * 4 + q) * 16 + (g > cols ? plane : 0) : sm100::smem_u32(&zero);
+    const int xstep = live ? p.group * 64 : 0, xplane = live ? plane : 0;
     int buf = 0;
     for (int tile = tile0 + team; tile < tile1; tile += teams) {
       // ---- this warp's cells of the tile
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      auto multiply = [&](uint4 wa, uint4 wb, uint32_t sa, uint32_t sb, uint32_t xat, bool down) {   // a cell's products
+      auto multiply = [&](uint4 wa, uint4 wb, uint32_t sa, uint32_t sb, uint32_t xat, auto down, auto pieces) {   // a cell's products
         float fa[4], fb[4];
         e8m0x4_to_f32(sa, fa);
         e8m0x4_to_f32(sb, fb);
@@ -571,12 +579,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
           float d[4];
           mma_f16_16816_zero(d, ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
           mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
-          if constexpr (kPieces == 2) {
+          if constexpr (decltype(pieces)::value) {
             const uint4 xl = lds128(xat + j * xstep + xplane);
             mma_f16_16816(d, ha[0], hb[0], ha[1], hb[1], xl.x, xl.y);
             mma_f16_16816(d, ha[2], hb[2], ha[3], hb[3], xl.z, xl.w);
           }
-          if (down) {
+          if constexpr (decltype(down)::value) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) d[k] *= xs1[k & 1];
           }
@@ -606,10 +614,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         load_next();
         if (++slot == kMvRing) slot = 0;
         const uint32_t xb = xlane + (cell0 + i) * 4 * xstep;
+        auto both = [&](auto pieces) {
 #pragma unroll
-        for (int c = 0; c < kMvCells; ++c) {
-          if (c > 0 && i + c >= mine) break;
-          multiply(wa[c], wb[c], sa[c], sb[c], xb + 4 * c * xstep, false);
+          for (int c = 0; c < kMvCells; ++c) {
+            if (c > 0 && i + c >= mine) break;
+            multiply(wa[c], wb[c], sa[c], sb[c], xb + 4 * c * xstep, std::false_type{}, pieces);
+          }
+        };
+        if constexpr (kDt == kF32) {
+          if (more) both(std::true_type{}); else both(std::false_type{});
+        } else {
+          both(std::false_type{});
         }
       }
       // ---- the sums lose the row's power of two.  Lifted by it they may have
@@ -630,7 +645,10 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         for (int i = 0; i < mine; ++i) {
           const uint4* wp = reinterpret_cast<const uint4*>(p.codes + (cell + i) * 1024) + lane;
           const uint32_t* sp = reinterpret_cast<const uint32_t*>(p.scales + (cell + i) * 64) + g;
-          multiply(__ldg(wp), __ldg(wp + 32), __ldg(sp), __ldg(sp + 8), xlane + (cell0 + i) * 4 * xstep, true);
+          const uint4 wa = __ldg(wp), wb = __ldg(wp + 32);
+          const uint32_t sa = __ldg(sp), sb = __ldg(sp + 8), xb = xlane + (cell0 + i) * 4 * xstep;
+          if (more) multiply(wa, wb, sa, sb, xb, std::true_type{}, std::true_type{});
+          else multiply(wa, wb, sa, sb, xb, std::true_type{}, std::false_type{});
         }
       }
       // ---- one warp of the team adds the partial sums in warp order and
@@ -647,6 +665,12 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
           t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
         }
         buf ^= 1;
+      }
+      if (packed) {                                            // columns c and c + 4: lanes q and q + 2
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, 2);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, 2);
+        t.z += __shfl_xor_sync(0xffffffffu, t.z, 2);
+        t.w += __shfl_xor_sync(0xffffffffu, t.w, 2);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

@@ -166,14 +166,13 @@ int launch_mv(MvArgs a, const DevInfo* d, cudaStream_t stream, bool after = fals
   static std::atomic<uint64_t> done{0};
   auto kern = fp4_matvec_kernel<kDt, kGated, kOut>;
   MX_TRY(ensure_smem(kern, done, 232448 - 1024));
-  constexpr int kPieces = kDt == kF32Two ? 2 : 1;
-  a.group = mv_group(a.K, a.E, a.S, kPieces);
+  a.group = mv_group(a.K, a.E, a.S, a.pieces);
   if (a.group == 0) return fail(MXMOE_ERR_SHAPE, "K=%d with E=%d and %d slots does not fit shared memory", a.K, a.E, a.S);
   // as many warps share a tile as leave each four cells or more of it
   a.team_log2 = kMvWarps % 4 == 0 ? 2 : 0;
   while (a.team_log2 > 0 && (4 << a.team_log2) > a.K / 128) --a.team_log2;
   const int grid = int(std::min<int64_t>(int64_t(a.S) * a.tiles, d->sms));
-  MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S, kPieces), stream, after, a), "4-bit matvec launch");
+  MX_CHECK_CUDA(launch_after(kern, dim3(grid), kMvThreads, mv_smem(a.K, a.group, a.E, a.S, a.pieces), stream, after, a), "4-bit matvec launch");
   return MXMOE_OK;
 }
 
@@ -393,6 +392,7 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
   a.ids = expert_ids;
   a.S = int(S);
   a.x_div = 1;
+  a.pieces = 1;
   a.E = E;
   a.tiles = int(N / 16);
   a.K = int(K);
@@ -422,7 +422,10 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   MX_TRY(check_mult("F", F, 128));
   if (D >= (1 << 24) || F >= (1 << 24) || S * (std::max(D, F) / 8) > 0x7FFFFFFF) return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld: too large", (long long)D, (long long)F);
   if (T == 0) return MXMOE_OK;
-  if (mv_group(D, E, int(S), 1) == 0 || mv_group(F, E, int(S), dtype == MXMOE_FP16 ? 2 : 1) == 0)
+  // h goes in as two f16 pieces; for a bf16 result as one (11 bits, an eighth of that
+  // result's rounding) where shared memory does not hold two of a row
+  const int pieces = dtype == MXMOE_BF16 && mv_group(F, E, int(S), 2) == 0 ? 1 : 2;
+  if (mv_group(D, E, int(S), 1) == 0 || mv_group(F, E, int(S), pieces) == 0)
     return fail(MXMOE_ERR_SHAPE, "D=%lld F=%lld with %lld slots does not fit shared memory", (long long)D, (long long)F, (long long)S);
   if (!qw) return fail(MXMOE_ERR_NULL, "qweights is NULL");
   MX_TRY(check_ptrs({{"x_tokens", x_tokens}, {"out_tokens", out_tokens}, {"qw.w13_codes", qw->w13_codes},
@@ -440,6 +443,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.S = int(S);
   a.E = E;
   // FC1 + SwiGLU: h [S, F] in fp32
+  a.pieces = 1;
   a.x = x_tokens;
   a.x_div = top_k;
   a.tiles = int(F / 8);
@@ -449,6 +453,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.out = ws.h;
   MX_TRY((dtype == MXMOE_BF16 ? launch_mv<kBF16, true, kF32>(a, d, stream) : launch_mv<kFP16, true, kF32>(a, d, stream)));
   // FC2: y [S, D] in fp32
+  a.pieces = pieces;
   a.x = ws.h;
   a.x_div = 1;
   a.tiles = int(D / 16);
@@ -456,7 +461,7 @@ int moe_layer_decode_fp4(const void* x_tokens, int64_t T, int64_t D, const int32
   a.codes = qw->w2_codes;
   a.scales = qw->w2_scales;
   a.out = ws.y;
-  MX_TRY((dtype == MXMOE_BF16 ? launch_mv<kF32, false, kF32>(a, d, stream, true) : launch_mv<kF32Two, false, kF32>(a, d, stream, true)));
+  MX_TRY((launch_mv<kF32, false, kF32>(a, d, stream, true)));
   const dim3 grid(unsigned((D / 4 + 127) / 128), unsigned(T));
   auto* o = static_cast<uint16_t*>(out_tokens);
   const auto combine = dtype == MXMOE_BF16 ? fp4_combine_kernel<kBF16> : fp4_combine_kernel<kFP16>;

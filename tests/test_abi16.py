@@ -140,3 +140,13 @@ def test_plain_forms_against_known_values():
     assert b[0, 0] == 127 and c[0].tolist() == [0x7E, 0x7E, 0xB8, 0x01]
     iw, isc = P16.fp4_tile_index(32, 256, False)
     assert sorted(iw.reshape(-1).tolist()) == list(range(32 * 32)) and sorted(isc.reshape(-1).tolist()) == list(range(32 * 8))
+
+
+def test_decode_sizes_that_shared_memory_holds(L):
+    """h goes in as two f16 pieces: fp16 layers are refused where a row of them does not fit, bf16 layers take one piece there."""
+    qw = mxk._Q4Weights(FAKE, FAKE, FAKE, FAKE)
+    f = lambda F, dt: L.moe_layer_decode_fp4(FAKE, 1, 128, FAKE, FAKE, 1, ctypes.byref(qw), 1, F, dt, FAKE, None, 0, None)  # noqa: E731
+    assert f(36224, 0) == f(36224, 1) == 8 and "workspace" in _err(L)          # fits; the workspace is missing
+    assert f(36352, 1) == 2 and "shared memory" in _err(L)
+    assert f(36352, 0) == 8 and f(72448, 0) == 8
+    assert f(72576, 0) == 2 and "shared memory" in _err(L)
