@@ -247,6 +247,11 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   auto tempty_bar = [&](int a) { return smem_u32(&bars[3 * C::kStages + 2 + a]); };
   auto info_bar = [&](int s) { return smem_u32(&bars[3 * C::kStages + 4 + s]); };
   auto seen_bar = [&](int s) { return smem_u32(&bars[3 * C::kStages + 4 + C::kInfo + s]); };
+  // Some waits last as long as a tile: the epilogue's and warp 3's for its last
+  // block, the producer's for a slot of the places when tiles without blocks follow
+  // it.  A block takes ~430 cycles, so an unsplit contraction of ten million of them
+  // is longer than the usual two seconds.
+  const long long whole = (1ll << 32) + 4096ll * (kMode == kWgrad ? (p.M + kBK - 1) / kBK : (p.kext + kBK - 1) / kBK);
   // A tile's place takes several hundred cycles to work out (a search, divisions).
   // The producer does it, tiles ahead, and the other roles of its CTA read it
   // (their i-th tile; ok: announced in time): 32768 rows x 8 x 4096 x 256 88 -> 82
@@ -254,7 +259,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
   // rows 119 -> 117.
   auto read_tile = [&](uint32_t i, bool& ok) {
     const int s = i % C::kInfo;
-    ok = __all_sync(0xffffffffu, mbar_wait(info_bar(s), (i / C::kInfo) & 1));
+    ok = __all_sync(0xffffffffu, mbar_wait(info_bar(s), (i / C::kInfo) & 1, whole));
     const uint4 a = lds128(sbase + C::OFF_INFO + s * C::INFO), b = lds128(sbase + C::OFF_INFO + s * C::INFO + 16);
     __syncwarp();
     if (lane == 0) mbar_arrive(seen_bar(s));
@@ -366,7 +371,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
     for (Walk<kMode> w(unit, units); w.tile() < ntiles && ok; w.next(), ++at) {
       const Tile T = get_tile<kMode>(p, offs, tab, ord, w.tile());
       const int slot = at % C::kInfo;
-      if (!__all_sync(0xffffffffu, mbar_wait(seen_bar(slot), ((at / C::kInfo) & 1) ^ 1))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, mbar_wait(seen_bar(slot), ((at / C::kInfo) & 1) ^ 1, whole))) { ok = false; break; }
       if (elect_one()) {
         const uint32_t to = sbase + C::OFF_INFO + slot * C::INFO;
         sts128(to, make_uint4(T.e | T.part << 16, T.kb0, T.kb1, T.r0));
@@ -468,7 +473,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
         stage = (stage + T.kb1 - T.kb0 - 1) % C::kStages;            // this unit's last block
         const int rem = T.len - (T.kb1 - 1) * kBK;
         if (rem < kBK && (rem & 15)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(stage), (used >> stage) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(stage), (used >> stage) & 1, whole));
           if (!ok) break;
           used ^= 1u << stage;
           // a K row is one 128-byte line of each box (the swizzle stays inside
@@ -521,7 +526,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
       const int row = T.r0 + rank * 128 + q * 32;                // this warp's 32 M-side rows
       const int chunks = (T.n + 31) >> 5;
       const bool any = T.kb1 != T.kb0;                           // kWgrad: an expert without rows has a zero gradient
-      if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase));
+      if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, whole));
       if (!(kPair ? pair_all(1 + pair, ok) : ok)) {             // (two that share a buffer leave together)
         if (lane == 0) raise_device_error(kErrTimeout);
         break;

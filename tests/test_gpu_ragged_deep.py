@@ -65,3 +65,27 @@ def test_weight_gradients_next_to_nan(E, mean, N, K, dt):
             else:
                 _same(out[e], (gr[s].t() @ a[s]).to(dt), f"expert {e} of {lens[e]} rows")
     assert mxk.device_error() == 0
+
+
+def test_a_contraction_of_seconds():
+    """An unsplit tile of 15.6 million K blocks (one expert's 10^9 rows, 38 experts, so no split) takes over three seconds: the
+    waits that last as long as the tile hold, and rows beyond 2^32 bytes are found.  Few rows are not zero, so sums are exact."""
+    M, E, N, K = 1_000_000_000, 38, 8, 8
+    assert mxk.ragged_workspace_bytes(M, N, K, E, 2) == 0
+    if torch.cuda.mem_get_info()[0] < 40 * 2 ** 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = _gen(2)
+    rows = torch.tensor([0, 1, 63, 64, 4_000_003, 2 ** 28 - 1, 2 ** 28, 2 ** 29 + 77, M - 14, M - 12, M - 11], device=DEV)
+    lens = [5] + [0] * 19 + [M - 5 - 11] + [0] * 16 + [11]          # the last expert's rows lie behind the long one's tail
+    off = P.offsets_of(lens)
+    x = torch.zeros(M, K, dtype=BF, device=DEV)
+    d = torch.zeros(M, N, dtype=BF, device=DEV)
+    vx, vd = _ints(g, rows.numel(), K), _ints(g, rows.numel(), N)
+    x[rows], d[rows] = vx.to(BF), vd.to(BF)
+    dw = mxk.mxmoe_ragged_gemm_wgrad(d, x, off.to(DEV))
+    for e in range(E):
+        s = (rows >= int(off[e])) & (rows < int(off[e + 1]))
+        _same(dw[e], (vd[s].t() @ vx[s]).to(BF), f"expert {e}")
+    del x, d
+    torch.cuda.empty_cache()
+    assert mxk.device_error() == 0
