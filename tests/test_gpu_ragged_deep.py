@@ -89,3 +89,29 @@ def test_a_contraction_of_seconds():
     del x, d
     torch.cuda.empty_cache()
     assert mxk.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("trans", [False, True], ids=["fwd", "dgrad"])
+@pytest.mark.parametrize("E,mean,rows,deep", [(24, 700, 4360, 328), (48, 60, 6664, 136), (24, 1100, 4104, 1288)])
+def test_products_of_many_tiles(E, mean, rows, deep, trans, dt):
+    """Blocks of eight row tiles (the last one short) over several token tiles, ragged in every dimension."""
+    g, lens = _gen(3), _lens(3, E, mean)
+    off = P.offsets_of(lens)
+    R, M = sum(lens), sum(lens) + 5
+    tiles = sum(-(-n // 256) for n in lens) * -(-rows // 256)
+    assert tiles > 16 * PAIRS and rows > 8 * 256
+    N, K = (deep, rows) if trans else (rows, deep)
+    a, w = _ints(g, M, deep), _ints(g, E, N, K).to(dt)
+    a[R:] = float("nan")
+    out = torch.full((M, rows), 7.0, dtype=dt, device=DEV)
+    x, o = a.to(dt), off.to(DEV)
+    for _ in range(2):
+        out.fill_(7.0)
+        mxk.mxmoe_ragged_gemm(x, w, o, transpose_w=trans, out=out)
+        for e in range(E):
+            s = slice(int(off[e]), int(off[e + 1]))
+            we = w[e].double()
+            _same(out[s], (a[s] @ (we if trans else we.t())).to(dt), f"expert {e} of {lens[e]} rows")
+        assert (out[R:] == 7).all()
+    assert mxk.device_error() == 0
