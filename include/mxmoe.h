@@ -606,14 +606,17 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *  x [S, K], y [S, N] 16-bit; weights [E, N, K] in the MXFP4_TILE layout;
  *  expert_ids DEVICE int32 [S] in [0, E) (any order, repeats allowed; an id
  *  outside raises MXMOE_ERR_ARG on the device and its row of y is not
- *  written).  Each expert's weights are read once per eight slots it has (fewer
- *  for K above 7168, as shared memory allows).  Products with f16 copies of x
+ *  written).  Each expert's weights are read once per group of eight of its slots;
+ *  a group is 4, 2 or 1 where shared memory does not hold more rows of x: it holds
+ *  2 K bytes a row of the group beside 16 bytes a slot, 4 an expert and 84 KB, in
+ *  226 KB (eight rows up to K = 8960 for 64 slots and experts, 6656 for 2048 slots
+ *  and 1024 experts).  Products with f16 copies of x
  *  (a power of two per row keeps every bit of an input that weighs 2^-36 of the
  *  row's largest value or more; an element is off by at most 2^-37 of it), fp32
  *  sums, one rounding.  Rows and scales of any size: a sum overflows only where
  *  one of the values themselves would in fp32.
  *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048, S * N / 16 < 2^31, and
- *  shared memory for one f16 row (K up to about 60000).
+ *  shared memory for one row (K up to 54016 at the largest S and E, 72448 at one).
  * ------------------------------------------------------------------------- */
 int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expert_ids, const uint8_t* codes,
                         const uint8_t* scales, int E, int64_t N, int dtype, void* y, cudaStream_t stream);
@@ -632,7 +635,9 @@ int mxfp4_expert_matvec(const void* x, int64_t S, int64_t K, const int32_t* expe
  *  of two per slot; where shared memory does not hold two of a row, F above 36224
  *  with one slot, bf16 layers take one piece and fp16 layers are refused); one
  *  rounding at the end.
- *  Needs D and F multiples of 128, T * top_k <= 2048, top_k <= E <= 1024.
+ *  Needs D and F multiples of 128, T * top_k <= 2048, top_k <= E <= 1024, and both
+ *  within mxfp4_expert_matvec's limit on K.  Rows of h take 4 F bytes there: groups
+ *  of eight up to F = 4480 for 64 slots and experts, 3328 at the largest.
  *  Workspace: mxfp4_decode_workspace_size() bytes, not shared by calls that
  *  may overlap on the GPU.
  * ------------------------------------------------------------------------- */

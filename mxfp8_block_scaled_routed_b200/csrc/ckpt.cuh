@@ -175,10 +175,12 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const CkptArgs p) 
     unpack8<kDt>(vd[i], d);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float s = sigmoid_fast(a[j]);
-      da[j] = d[j] * b[j] * s * (1.0f + a[j] * (1.0f - s));
-      db[j] = d[j] * a[j] * s;
-      h[j] = a[j] * s * b[j];
+      // (the factors of the gate first: they lie in [-0.1, 1.1] and [-0.3, a], and
+      // dh b or dh a alone could overflow and meet a zero)
+      const float s = sigmoid_fast(a[j]), silu = a[j] * s;
+      da[j] = d[j] * (s * (1.0f + a[j] * (1.0f - s))) * b[j];
+      db[j] = d[j] * silu;
+      h[j] = silu * b[j];
     }
     uint16_t* g = p.dh13 + row * 2 * p.F + c;
     *reinterpret_cast<uint4*>(g) = pack8<kDt>(da);

@@ -150,3 +150,11 @@ def test_decode_sizes_that_shared_memory_holds(L):
     assert f(36352, 1) == 2 and "shared memory" in _err(L)
     assert f(36352, 0) == 8 and f(72448, 0) == 8
     assert f(72576, 0) == 2 and "shared memory" in _err(L)
+
+
+def test_matvec_sizes_that_shared_memory_holds(L):
+    """The header's limits on K: at the largest S and E, and at one."""
+    f = lambda K, S, E: L.mxfp4_expert_matvec(None, S, K, FAKE, FAKE, FAKE, E, 16, 0, FAKE, None)  # noqa: E731
+    for K, S, E in ((54016, 2048, 1024), (72448, 1, 1)):
+        assert f(K, S, E) == 1 and "x is NULL" in _err(L)          # fits; refused for its pointer
+        assert f(K + 128, S, E) == 2 and "shared memory" in _err(L)

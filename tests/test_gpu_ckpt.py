@@ -165,3 +165,27 @@ def test_no_rows():
     assert o["h"].shape == (0, 32)
     g = mxk.mxfp8_swiglu_ckpt_bwd(torch.empty(0, 32, dtype=BF, device=DEV), o["codes"], o["scales"])
     assert g["dh13"].shape == (0, 64)
+
+
+def test_large_gradients_of_far_gates():
+    """dh up beyond fp32 where the gate's factor is zero or small: the gradients are what the formula gives, not NaN."""
+    F = 32
+    gates = torch.tensor([-3e38, -1e30, -200.0, -90.0, -60.0, -30.0, 0.0, 3.0])
+    h13 = torch.cat([gates.unsqueeze(1).expand(8, F), torch.full((8, F), 2.0 ** 80)], dim=1).to(BF)
+    dh = torch.full((8, F), 2.0 ** 60, dtype=BF)
+    out = mxk.mxfp8_swiglu_ckpt(h13.to(DEV))
+    got = mxk.mxfp8_swiglu_ckpt_bwd(dh.to(DEV), out["codes"], out["scales"])
+    a, b = _kept(out["codes"], out["scales"], F)
+    d, s = dh.double(), P.sigmoid(a)
+    t = s * (1 + a * (1 - s))
+    da, db = (d * t * b).to(BF).double(), (d * a * s).to(BF).double()
+    # the sigmoid's own error and its flush below 2^-126 (S0), as above; beyond bf16's range: the same infinity
+    r = P.sigmoid_err(a) + 2.0 ** -20
+    for x, y, m, what in ((got["dh13"][:, :F], da, d * b, "da"), (got["dh13"][:, F:], db, d * a, "db")):
+        x = x.cpu().double()
+        assert not torch.isnan(x).any(), what
+        big = ~torch.isfinite(y)
+        assert torch.equal(x[big], y[big]), what
+        # (the bracket's own relative error is up to |a| times the sigmoid's)
+        e = torch.nan_to_num((2 * r * (1 + a.abs()) + 2 * P.u(BF)) * y.abs(), posinf=0.0) + S0 * (m.abs().clamp(max=2.0 ** 200) * (1 + a.abs().clamp(max=200.0)) + 1)
+        P.assert_within(x[~big], y[~big], e[~big], what)
