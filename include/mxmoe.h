@@ -613,8 +613,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
  *  and 1024 experts).  Products with f16 copies of x
  *  (a power of two per row keeps every bit of an input that weighs 2^-36 of the
  *  row's largest value or more; an element is off by at most 2^-37 of it), fp32
- *  sums, one rounding.  Rows and scales of any size: a sum overflows only where
- *  one of the values themselves would in fp32.
+ *  sums, one rounding.  Rows and scales may have any size: a sum overflows only
+ *  where the fp32 sum of the products themselves would.
  *  Needs K % 128 == 0, N % 16 == 0, E <= 1024, S <= 2048, S * N / 16 < 2^31, and
  *  shared memory for one row (K up to 54016 at the largest S and E, 72448 at one).
  * ------------------------------------------------------------------------- */

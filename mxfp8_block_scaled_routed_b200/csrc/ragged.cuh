@@ -33,8 +33,8 @@
 // tile's epilogue runs beside the next tile's MMAs.
 //
 // Bound by the MMAs (512 cycles a full K block) from about ten K blocks a tile
-// on, and in a loop by the power limit (49152 rows, 64 x 2816 x 2048: 440 us,
-// 1.29 PFLOP/s).  Shorter tiles wait for their stores: a chunk's staging buffer
+// on, and in a long loop by the power limit (49152 rows, 64 x 2816 x 2048: 412 to
+// 440 us in a short loop, 1.29 to 1.38 PFLOP/s; 505 to 523 in a long one).  Shorter tiles wait for their stores: a chunk's staging buffer
 // is free 300 to 490 cycles late while the tiles' loads and stores together move
 // 11 TB/s through L2 (32768 rows, 8 x 4096 x 256: 73 us, ~3,700 cycles a tile of
 // 2,048 of MMAs; long contractions load 13 TB/s).  Few tiles with a long
@@ -492,8 +492,7 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
           // orders them before lane 0's release, and that one has to be of cluster
           // scope to pair with the issuer's acquire.  Only shared memory is
           // published: a release of all state spaces waits for the stores under way
-          // (64 experts of 760 rows x 2816 x 2048 463 us against 423, 64 of 94 rows
-          // x 2048 x 2048 146 against 136)
+          // (64 experts of 760 rows x 2816 x 2048 463 us against 412)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive_release_shared(full_bar(stage), 0);
