@@ -18,7 +18,7 @@ def test_differences_of_neighbouring_h_survive(T, dt):
     """Pairs of h near 2^17 that differ by 32, and second weights that subtract them: the layer's result is that difference.
     Eleven bits of h would leave steps of 64 to 128.  Slots of one expert from one to a full group of eight and beyond.
 
-    x = 1, gates 32, ups 3072 + r and 3072 + r + 1 (whole numbers, exact in fp32), so h = 32 s up with s = 1 - e^-32: each is off
+    x = 1, gates 32, ups 6 * 2^9 + r and one more (whole numbers, exact in fp32), so h = 32 s up with s = 1 - e^-32: each is off
     by at most (6 + 1.2 * 32) 2^-23 + 2^-22 for the sigmoid and the products and 2^-22 for the pieces, and the result by twice that."""
     r = np.random.default_rng(41)
     E, D, F = 2, 128, 128
